@@ -32,10 +32,15 @@ MTGR_ERR_RANGE = 7
 MTGR_F32 = 0
 MTGR_BF16 = 1
 MTGR_F16 = 2
+MTGR_I8 = 3  # signed bytes with a scale per row; only the int8 operators take it
 
 MTGR_EPI_NONE = 0
 MTGR_EPI_SILU = 1
 MTGR_EPI_RESID = 2
+
+MTGR_GATE_NONE = 0
+MTGR_GATE_LINEAR = 1
+MTGR_GATE_SILU = 2
 
 TILE_M = 128
 TILE_N = 128
@@ -86,6 +91,21 @@ class MtgrTokenMlp(ctypes.Structure):
 class MtgrHeadParams(ctypes.Structure):
     _fields_ = [("d", c_i32), ("d_h", c_i32), ("n_tasks", c_i32), ("reserved", c_i32),
                 ("w1", c_vp), ("b1", c_vp), ("w2", c_vp), ("b2", c_vp)]
+
+
+class MtgrBoundaryParams(ctypes.Structure):
+    _fields_ = [("d", c_i32), ("G", c_i32), ("eps", c_float), ("gate", c_i32),
+                ("post_gamma", c_vp), ("post_beta", c_vp), ("scale", c_vp), ("pre_gamma", c_vp),
+                ("pre_beta", c_vp)]
+
+
+class MtgrBoundaryGrads(ctypes.Structure):
+    _fields_ = [("post_gamma", c_vp), ("post_beta", c_vp), ("scale", c_vp), ("pre_gamma", c_vp),
+                ("pre_beta", c_vp)]
+
+
+class MtgrGradTensor(ctypes.Structure):
+    _fields_ = [("g", c_vp), ("out", c_vp), ("n", c_i64), ("dtype", c_i32), ("out_dtype", c_i32)]
 
 
 _SIGNATURES = {
@@ -152,6 +172,21 @@ _SIGNATURES = {
     "mtgr_hstu_block_bwd": (ctypes.c_int, [ctypes.POINTER(MtgrBlockParams),
                                            ctypes.POINTER(MtgrBatch), c_vp, c_vp, c_vp, c_vp,
                                            ctypes.POINTER(MtgrBlockGrads), c_vp, c_size, c_vp]),
+    "mtgr_boundary_fwd": (ctypes.c_int, [c_vp, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32,
+                                         c_vp, c_vp, c_i32, c_vp, c_vp, c_vp]),
+    "mtgr_boundary_bwd_workspace_bytes": (c_size, [c_i32, c_vp]),
+    "mtgr_boundary_bwd": (ctypes.c_int, [c_vp, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32,
+                                         c_vp, c_vp, c_i32, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                         c_vp, c_vp, c_size, c_vp, c_vp]),
+    "mtgr_quantize_rows": (ctypes.c_int, [c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_vp]),
+    "mtgr_gemm_i8": (ctypes.c_int, [c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
+                                    c_i32, c_i32, c_vp, c_vp, c_vp]),
+    "mtgr_linear_i8_workspace_bytes": (c_size, [c_i32, c_i32]),
+    "mtgr_linear_i8": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_vp,
+                                      c_i32, c_vp, c_i32, c_i32, c_vp, c_vp, c_size, c_vp, c_vp]),
+    "mtgr_grad_clip_workspace_bytes": (c_size, [c_vp, c_i32]),
+    "mtgr_grad_clip": (ctypes.c_int, [c_vp, c_i32, c_float, c_float, c_vp, c_vp, c_size, c_vp,
+                                      c_vp]),
 }
 
 _lib = None
@@ -431,3 +466,74 @@ def mtgr_stack_fwd_host(layers, h_lens, h_ts, h_norm, h_x_in, h_x_out, h_status,
         arr, len(layers), int(h_lens.shape[0]), _ptr(h_lens), _ptr(h_ts), _ptr(h_norm),
         _ptr(h_x_in), _ptr(h_x_out), _ptr(h_status), _ptr(d_ws),
         d_ws.numel() * d_ws.element_size(), _stream(stream)))
+
+
+def _i8_dtype(t: torch.dtype) -> int:
+    return MTGR_I8 if t == torch.int8 else dtype_code(t)
+
+
+def mtgr_boundary_fwd(p: MtgrBoundaryParams, T, d_group_id, d_o, d_u, d_x, d_h, d_y, d_y_scale,
+                      stream=None) -> None:
+    """d_u None without a gate; d_y and d_y_scale None without the pre norm (d_y_scale: int8 d_y)."""
+    _check("mtgr_boundary_fwd", load().mtgr_boundary_fwd(
+        ctypes.byref(p), T, _ptr(d_group_id), dtype_code(d_o.dtype), _ptr(d_o), d_o.stride(0),
+        _ptr(d_u), 0 if d_u is None else d_u.stride(0), dtype_code(d_x.dtype), _ptr(d_x), _ptr(d_h),
+        MTGR_F32 if d_y is None else _i8_dtype(d_y.dtype), _ptr(d_y), _ptr(d_y_scale),
+        _stream(stream)))
+
+
+def mtgr_boundary_bwd_workspace_bytes(T: int, p: MtgrBoundaryParams) -> int:
+    return load().mtgr_boundary_bwd_workspace_bytes(T, ctypes.byref(p))
+
+
+def mtgr_boundary_bwd(p: MtgrBoundaryParams, T, d_group_id, d_o, d_u, d_x, d_dh, d_dy, d_do, d_du, d_dx,
+                      grads: MtgrBoundaryGrads, d_ws, d_status=None, stream=None) -> None:
+    _check("mtgr_boundary_bwd", load().mtgr_boundary_bwd(
+        ctypes.byref(p), T, _ptr(d_group_id), dtype_code(d_o.dtype), _ptr(d_o), d_o.stride(0),
+        _ptr(d_u), 0 if d_u is None else d_u.stride(0), dtype_code(d_dx.dtype), _ptr(d_x),
+        _ptr(d_dh), MTGR_F32 if d_dy is None else dtype_code(d_dy.dtype), _ptr(d_dy), _ptr(d_do),
+        d_do.stride(0), _ptr(d_du), 0 if d_du is None else d_du.stride(0), _ptr(d_dx),
+        ctypes.byref(grads), _ptr(d_ws), d_ws.numel() * d_ws.element_size(), _ptr(d_status),
+        _stream(stream)))
+
+
+def mtgr_quantize_rows(d_x, d_q, d_scale, stream=None) -> None:
+    M, K = d_x.shape
+    _check("mtgr_quantize_rows", load().mtgr_quantize_rows(
+        M, K, dtype_code(d_x.dtype), _ptr(d_x), d_x.stride(0), _ptr(d_q), _ptr(d_scale),
+        _stream(stream)))
+
+
+def mtgr_gemm_i8(d_a, d_a_scale, d_b, d_b_scale, d_bias, epi, d_resid, q_cols, d_out, d_status,
+                 stream=None) -> None:
+    M, K = d_a.shape
+    _check("mtgr_gemm_i8", load().mtgr_gemm_i8(
+        M, d_b.shape[0], K, _ptr(d_a), _ptr(d_a_scale), _ptr(d_b), _ptr(d_b_scale), _ptr(d_bias),
+        epi, _ptr(d_resid), q_cols, dtype_code(d_out.dtype), _ptr(d_out), _ptr(d_status),
+        _stream(stream)))
+
+
+def mtgr_linear_i8_workspace_bytes(M: int, K: int) -> int:
+    return load().mtgr_linear_i8_workspace_bytes(M, K)
+
+
+def mtgr_linear_i8(d_x, d_w, d_w_scale, d_bias, epi, d_resid, q_cols, d_out, d_ws, d_status,
+                   stream=None) -> None:
+    M, K = d_x.shape
+    _check("mtgr_linear_i8", load().mtgr_linear_i8(
+        M, d_w.shape[0], K, dtype_code(d_x.dtype), _ptr(d_x), d_x.stride(0), _ptr(d_w),
+        _ptr(d_w_scale), _ptr(d_bias), epi, _ptr(d_resid), q_cols, dtype_code(d_out.dtype),
+        _ptr(d_out), _ptr(d_ws), d_ws.numel() * d_ws.element_size(), _ptr(d_status),
+        _stream(stream)))
+
+
+def mtgr_grad_clip_workspace_bytes(h_grads, n: int) -> int:
+    """h_grads: a ctypes array of MtgrGradTensor."""
+    return load().mtgr_grad_clip_workspace_bytes(h_grads, n)
+
+
+def mtgr_grad_clip(h_grads, n: int, max_norm: float, inv_scale: float, d_norm, d_ws, d_status,
+                   stream=None) -> None:
+    _check("mtgr_grad_clip", load().mtgr_grad_clip(
+        h_grads, n, max_norm, inv_scale, _ptr(d_norm), _ptr(d_ws),
+        d_ws.numel() * d_ws.element_size(), _ptr(d_status), _stream(stream)))

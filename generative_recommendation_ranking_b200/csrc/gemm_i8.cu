@@ -1,0 +1,462 @@
+// Product of signed bytes with a scale per row of a (token) and per row of b
+// (output channel) on the 5th-generation tensor cores, with the block's
+// epilogues (the projections of the summary page's "Method" block update):
+//
+//   out[m][n] = epi(sa[m] sb[n] sum_k a[m][k] b[n][k] + bias[n])
+//
+// The sums are exact (int32 accumulators in TMEM, K <= 131072); the scales, the
+// bias and the epilogue are applied in fp32 and rounded once.
+//
+// Design: persistent warp-specialised kernel as for the bf16 product: TMA loads of
+// 128-byte k-blocks (128-byte swizzle) through an mbarrier ring, one thread
+// issuing tcgen05.mma kind::i8 (K = 32 per instruction, twice the bf16 rate), and
+// epilogue warps that drain a double-buffered accumulator, stage 32 x 32 blocks in
+// swizzled shared memory and leave them by TMA stores.
+//   CG = 2: CTA pairs, 256 x 256 tiles (an SM reads its 128 rows of a and half of
+//           the 256 columns of b): many rows.
+//   CG = 1: one CTA, 128 x 64 tiles, so that a few hundred rows spread over the SMs.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "ops.h"
+#include "ptx.cuh"
+#include "tmap.h"
+
+namespace mtgr {
+
+namespace {
+
+constexpr int BM = 128;   // rows of a per CTA
+constexpr int BK = 128;   // bytes of k per stage: one swizzle row
+constexpr int A_BYTES = BM * BK;
+
+template <int CG>
+struct Shape {
+  static constexpr int kBN = CG == 2 ? 256 : 64;   // columns of a tile
+  static constexpr int kBRows = kBN / CG;          // rows of b per CTA
+  static constexpr int kBBytes = kBRows * BK;
+  static constexpr int kStageBytes = A_BYTES + kBBytes;
+  static constexpr int kStages = 6;
+  static constexpr int kTileM = BM * CG;
+  static constexpr int kTmemCols = 2 * kBN;
+};
+
+// Epilogue warps: eight (two per TMEM lane quarter) for the 16-bit outputs of the
+// pair form, whose main loop is short; four otherwise. Two staging blocks each.
+template <int OUT, int CG>
+struct Epi {
+  static constexpr int kWarps = CG == 2 && OUT != MTGR_F32 ? 8 : 4;
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kStg = OUT == MTGR_F32 ? 4096 : 2048;
+  static constexpr size_t kSmem = 1024 + (size_t)Shape<CG>::kStages * Shape<CG>::kStageBytes +
+                                  (size_t)kWarps * 2 * kStg + 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+};
+
+struct Args {
+  int M, N, K;
+  const float* sa;
+  const float* sb;
+  const float* bias;
+  const float* resid;
+  int q_cols;
+  int32_t* status;
+};
+
+// Instruction descriptor of tcgen05.mma kind::i8: D int32 (2 at bits 4-5), A and
+// B signed bytes (1 at 7-9 and 10-12), both K-major, N >> 3 at 17, M >> 4 at 24.
+constexpr uint32_t idesc_i8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if constexpr (CG == 2) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// 16-byte chunk c of row r of a staging block (64-byte swizzle for 16-bit rows of
+// 32, 128-byte for fp32 ones)
+template <int OUT>
+__device__ __forceinline__ uint32_t stg_off(int r, int c) {
+  return OUT == MTGR_F32 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4))
+                         : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// 32 columns [col0, col0 + 32) of one row: scales, bias, epilogue, to the staging
+// block. Columns past N (N % 8 == 0) are not stored: their scales are not read.
+template <int EPI, int OUT>
+__device__ __forceinline__ void epilogue_block(const Args& a, int col0, float sa, const uint32_t (&acc)[32],
+                                               const float4 (&res)[8], uint8_t* stg, int r) {
+  float v[32];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    float4 sb = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col0 + 4 * c < a.N) sb = __ldg(reinterpret_cast<const float4*>(a.sb + col0) + c);
+    v[4 * c] = __int2float_rn((int)acc[4 * c]) * sa * sb.x;
+    v[4 * c + 1] = __int2float_rn((int)acc[4 * c + 1]) * sa * sb.y;
+    v[4 * c + 2] = __int2float_rn((int)acc[4 * c + 2]) * sa * sb.z;
+    v[4 * c + 3] = __int2float_rn((int)acc[4 * c + 3]) * sa * sb.w;
+  }
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (col0 + 4 * c < a.N) {
+        const float4 b4 = __ldg(reinterpret_cast<const float4*>(a.bias + col0) + c);
+        v[4 * c] += b4.x; v[4 * c + 1] += b4.y; v[4 * c + 2] += b4.z; v[4 * c + 3] += b4.w;
+      }
+    }
+  }
+  if (EPI == MTGR_EPI_SILU) {
+    // v / (1 + e^-v): a tanh approximation would leave the small values of
+    // negative v with only a few right bits
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = __fdividef(v[c], 1.0f + __expf(-v[c]));
+  }
+  if (EPI == MTGR_EPI_RESID) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      v[4 * c] += res[c].x; v[4 * c + 1] += res[c].y; v[4 * c + 2] += res[c].z; v[4 * c + 3] += res[c].w;
+    }
+  }
+  if (col0 < a.q_cols) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] *= 0.5f;
+  }
+  if (OUT == MTGR_F16) {
+    // the conversion saturates: a value beyond f16 is reported
+    float m = 0.f;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) m = fmaxf(m, fabsf(v[c]));
+    if (__any_sync(0xffffffffu, m > 65504.f) && (threadIdx.x & 31) == 0)
+      set_status(a.status, MTGR_ERR_RANGE);
+  }
+  if (OUT == MTGR_F32) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<float4*>(stg + stg_off<OUT>(r, c)) =
+          make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float lo = v[8 * c + 2 * k], hi = v[8 * c + 2 * k + 1];
+        w[k] = OUT == MTGR_F16 ? cvt_f16x2(lo, hi) : cvt_bf16x2(lo, hi);
+      }
+      *reinterpret_cast<uint4*>(stg + stg_off<OUT>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+template <int EPI, int OUT, int CG>
+__global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
+    gemm_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmO, Args args) {
+  using S = Shape<CG>;
+  using E = Epi<OUT, CG>;
+  constexpr int NST = S::kStages, BN = S::kBN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + NST * A_BYTES;
+  uint8_t* sStg = sB + NST * S::kBBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sStg + E::kWarps * 2 * E::kStg);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + NST;
+  uint64_t* acc_full = bars + 2 * NST;
+  uint64_t* acc_empty = bars + 2 * NST + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 4);
+
+  const int warp = warp_id(), lane = lane_id();
+  const int M = args.M, N = args.N;
+  const int n_tiles = (N + BN - 1) / BN;
+  const int num_tiles = ((M + S::kTileM - 1) / S::kTileM) * n_tiles;
+  const int kblocks = (args.K + BK - 1) / BK;  // a ragged last block is zero-filled by the loads
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  const int tile0 = CG == 2 ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int tstride = CG == 2 ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmO);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], CG * E::kWarps);  // the pair's epilogue warps, on the leader's barrier
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    if constexpr (CG == 2) {
+      tmem_alloc_cg2(tmem_slot, S::kTmemCols);
+      tmem_relinquish_cg2();
+    } else {
+      tmem_alloc(tmem_slot, S::kTmemCols);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  if constexpr (CG == 2) cluster_sync();
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  bool timed_out = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int tile = tile0; tile < num_tiles && !timed_out; tile += tstride) {
+        const int mb = tile / n_tiles, nb = tile % n_tiles;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1)) { timed_out = true; break; }
+          uint8_t* da = sA + stage * A_BYTES;
+          uint8_t* db = sB + stage * S::kBBytes;
+          const int ya = mb * S::kTileM + (int)rank * BM, yb = nb * BN + (int)rank * S::kBRows;
+          if constexpr (CG == 2) {
+            // both CTAs' halves complete on the leader's barrier, which the
+            // leader arms for the bytes of both
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
+            const uint32_t fb = mapa_shared(&full[stage], 0);
+            tma_load_2d_cg2(&tmA, fb, da, kb * BK, ya);
+            tma_load_2d_cg2(&tmB, fb, db, kb * BK, yb);
+          } else {
+            mbar_arrive_expect_tx(&full[stage], S::kStageBytes);
+            tma_load_2d(&tmA, &full[stage], da, kb * BK, ya);
+            tma_load_2d(&tmB, &full[stage], db, kb * BK, yb);
+          }
+          if (++stage == NST) { stage = 0; phase ^= 1; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_i8(S::kTileM, BN);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      for (int tile = tile0; tile < num_tiles && !timed_out; tile += tstride) {
+        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1)) { timed_out = true; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BN;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(&full[stage], phase)) { timed_out = true; break; }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(sA + stage * A_BYTES);
+          const uint32_t b_addr = smem_u32(sB + stage * S::kBBytes);
+#pragma unroll
+          for (int k = 0; k < BK / 32; ++k)
+            mma_i8<CG>(d_tmem, sdesc_sw128(a_addr + 32 * k, 16, 1024), sdesc_sw128(b_addr + 32 * k, 16, 1024),
+                       idesc, (kb | k) != 0 ? 1u : 0u);
+          if constexpr (CG == 2) tc_commit_cg2(&empty[stage], 0x3);
+          else tc_commit(&empty[stage]);
+          if (++stage == NST) { stage = 0; phase ^= 1; }
+        }
+        if (timed_out) break;
+        if constexpr (CG == 2) tc_commit_cg2(&acc_full[acc], 0x3);
+        else tc_commit(&acc_full[acc]);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+      }
+    }
+  } else {
+    // epilogue warp ew drains rows [32 quarter, 32 quarter + 32) of its CTA,
+    // the blocks of its column group
+    const int quarter = warp & 3, ew = warp - 2;
+    constexpr int NB = (BN / 32) / (E::kWarps / 4);  // blocks a warp drains per tile
+    const int grp = ew >> 2;
+    uint8_t* stg = sStg + ew * 2 * E::kStg;
+    int acc = 0;
+    uint32_t acc_phase = 0, chunk = 0;
+    // the residual comes by plain loads into a ring of two blocks, ahead of use
+    // and across tile boundaries, so that its latency hides behind the drain
+    constexpr int RB = EPI == MTGR_EPI_RESID ? 2 : 1;
+    static_assert(EPI != MTGR_EPI_RESID || NB % RB == 0, "a block's ring slot is its index mod RB");
+    float4 rs[RB][8];
+    int lt = tile0, lc = 0;  // the next block to load
+    auto load_next = [&](float4 (&z)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (lt < num_tiles) {
+        const int m = (lt / n_tiles) * S::kTileM + (int)rank * BM + quarter * 32 + lane;
+        const int col = (lt % n_tiles) * BN + (grp * NB + lc) * 32;
+        if (m < M) {
+          const float4* p = reinterpret_cast<const float4*>(args.resid + (size_t)m * N + col);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (col + 4 * i < N) z[i] = __ldg(p + i);
+        }
+      }
+      if (++lc == NB) { lc = 0; lt += tstride; }
+    };
+    if constexpr (EPI == MTGR_EPI_RESID) {
+#pragma unroll
+      for (int sl = 0; sl < RB; ++sl) load_next(rs[sl]);
+    }
+    for (int tile = tile0; tile < num_tiles; tile += tstride) {
+      const int mb = tile / n_tiles, nb = tile % n_tiles;
+      const int row0 = mb * S::kTileM + (int)rank * BM + quarter * 32;
+      const float sa = row0 + lane < M ? __ldg(args.sa + row0 + lane) : 0.f;
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase));
+      if (!ok) { timed_out = true; break; }
+      tc_fence_after();
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
+#pragma unroll RB
+      for (int cc = 0; cc < NB; ++cc) {
+        const int col0 = nb * BN + (grp * NB + cc) * 32;
+        if (col0 < N) {
+          uint8_t* sb = stg + (chunk & 1) * E::kStg;
+          // the TMA store that last read this buffer (two blocks ago) must be done
+          if (lane == 0) bulk_wait_group_read<1>();
+          __syncwarp();
+          uint32_t r[32];
+          tmem_ld32(t_row + (grp * NB + cc) * 32, r);
+          tmem_ld_wait();
+          epilogue_block<EPI, OUT>(args, col0, sa, r, rs[cc % RB], sb, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmO, sb, col0, row0);
+            bulk_commit_group();
+          }
+          ++chunk;
+        }
+        if constexpr (EPI == MTGR_EPI_RESID) load_next(rs[cc % RB]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        // the accumulator is released on the leader's barrier (its TMEM loads
+        // have completed, so the remote arrive needs no ordering)
+        if (CG == 1 || rank == 0) mbar_arrive(&acc_empty[acc]);
+        else mbar_arrive_cluster_relaxed(mapa_shared(&acc_empty[acc], 0));
+      }
+      if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+    }
+    if (lane == 0) bulk_wait_group<0>();  // stores complete before the CTA retires
+  }
+  if (timed_out) set_status(args.status, MTGR_ERR_TIMEOUT);
+  // a pair retires together: the leader's MMAs read the other CTA's shared
+  // memory and the other CTA arrives on the leader's barriers
+  tc_fence_before();
+  if constexpr (CG == 2) cluster_sync();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (CG == 2) tmem_dealloc_cg2(tmem_base, S::kTmemCols);
+    else tmem_dealloc(tmem_base, S::kTmemCols);
+  }
+}
+
+constexpr int kMaxDevices = 64;
+
+template <int EPI, int OUT, int CG>
+int launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const Args& args,
+             cudaStream_t s) {
+  using E = Epi<OUT, CG>;
+  auto kern = gemm_i8_kernel<EPI, OUT, CG>;
+  // per device: blocks (pairs) resident at once; 0 until the first launch there
+  static std::atomic<int> resident[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MTGR_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(E::kThreads);
+  cfg.dynamicSmemBytes = E::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 1 : 0;
+  int units = resident[dev].load(std::memory_order_relaxed);
+  if (units == 0) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)E::kSmem) != cudaSuccess)
+      return MTGR_ERR_CUDA;
+    units = device_sm_count();
+    if (CG == 2) {  // a GPC with an odd number of SMs leaves one unpaired
+      cfg.gridDim = dim3(units);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) return MTGR_ERR_CUDA;
+      units = n;
+    }
+    resident[dev].store(units, std::memory_order_relaxed);
+  }
+  const int64_t tiles = (((int64_t)args.M + BM * CG - 1) / (BM * CG)) *
+                        ((args.N + Shape<CG>::kBN - 1) / Shape<CG>::kBN);
+  if (tiles > 0x3fffffff) return MTGR_ERR_UNSUPPORTED;  // the kernel counts tiles in 32 bits
+  cfg.gridDim = dim3((unsigned)(CG * (tiles < units ? tiles : units)));
+  if (cudaLaunchKernelEx(&cfg, kern, ta, tb, to, args) != cudaSuccess) return MTGR_ERR_CUDA;
+  return launch_status();
+}
+
+template <int CG>
+int launch_cg(int M, int N, int K, const int8_t* a, const int8_t* b, int epi, int32_t out_dtype, void* out,
+              const Args& args, cudaStream_t s) {
+  using S = Shape<CG>;
+  CUtensorMap ta, tb, to;
+  int rc = make_tmap_2d(&ta, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)M, (uint64_t)K, BK, BM,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != MTGR_OK) return rc;
+  rc = make_tmap_2d(&tb, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)N, (uint64_t)K, BK,
+                    S::kBRows, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != MTGR_OK) return rc;
+  rc = out_dtype == MTGR_F32
+           ? make_tmap_2d(&to, out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (uint64_t)N, (uint64_t)M,
+                          (uint64_t)N * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B)
+           : make_tmap_2d(&to, out, CU_TENSOR_MAP_DATA_TYPE_UINT16, (uint64_t)N, (uint64_t)M,
+                          (uint64_t)N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+  if (rc != MTGR_OK) return rc;
+#define MTGR_FORM(E, O) \
+  if (epi == E && out_dtype == O) return launch_t<E, O, CG>(ta, tb, to, args, s)
+  MTGR_FORM(MTGR_EPI_NONE, MTGR_F16);
+  MTGR_FORM(MTGR_EPI_NONE, MTGR_BF16);
+  MTGR_FORM(MTGR_EPI_NONE, MTGR_F32);
+  MTGR_FORM(MTGR_EPI_SILU, MTGR_F16);
+  MTGR_FORM(MTGR_EPI_SILU, MTGR_BF16);
+  MTGR_FORM(MTGR_EPI_SILU, MTGR_F32);
+  MTGR_FORM(MTGR_EPI_RESID, MTGR_F32);
+#undef MTGR_FORM
+  return MTGR_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+// K % 16 == 0, N % 8 == 0, 16-byte aligned operands.
+int launch_gemm_i8(int M, int N, int K, const int8_t* a, const float* sa, const int8_t* b, const float* sb,
+                   const float* bias, int epi, const float* resid, int q_cols, int32_t out_dtype, void* out,
+                   int32_t* status, cudaStream_t s) {
+  if (M == 0 || N == 0) return MTGR_OK;
+  const Args args{M, N, K, sa, sb, bias, resid, q_cols, status};
+  // pair tiles once they fill every SM; below, the small tiles spread the work
+  const int64_t pair_tiles = (((int64_t)M + 255) / 256) * ((N + 255) / 256);
+  if (2 * pair_tiles >= device_sm_count()) return launch_cg<2>(M, N, K, a, b, epi, out_dtype, out, args, s);
+  return launch_cg<1>(M, N, K, a, b, epi, out_dtype, out, args, s);
+}
+
+}  // namespace mtgr

@@ -1,0 +1,258 @@
+// The global 2-norm over many gradient tensors, the loss scale taken out, and
+// clipping (the block's gradients, of a loss that f16 training scales):
+//   norm = inv_scale sqrt(sum g^2),  c = inv_scale min(1, max_norm / (norm + 1e-6)),  out = g c
+// Two kernels over all tensors: the first sums squares (each gradient read once),
+// the second scales (read again, from L2 where the set fits, and written). The
+// tensors travel as a table in the kernel's parameters, so nothing is copied to
+// the device ahead. Bound by HBM.
+//
+// Sums: squares of eight values in fp32, over those in fp64; where the eight
+// leave fp32's range (values beyond 1e18 or all below 1e-18), they are squared in
+// fp64. Blocks write their sums to the workspace and the second kernel adds
+// them in a fixed order: no atomics, the same norm in every run.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "ops.h"
+#include "rowvec.cuh"
+
+namespace mtgr {
+
+namespace {
+
+constexpr int kTable = 96;            // tensors per launch
+constexpr int64_t kChunk = 16384;     // elements a block takes at a time
+
+struct Table {
+  const void* g[kTable];
+  void* out[kTable];
+  int64_t n[kTable];
+  int32_t chunk0[kTable + 1];  // first chunk of each tensor
+  uint8_t dtype[kTable];       // in | out << 4
+  int32_t count;
+};
+
+__device__ __forceinline__ int find_tensor(const Table& t, int chunk) {
+  int lo = 0, hi = t.count - 1;  // the last tensor whose first chunk is <= chunk
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.chunk0[mid] <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double square8(const float (&v)[8]) {
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s = fmaf(v[e], v[e], s);
+  if (s > 1e-30f && s < 1e36f) return (double)s;  // no square that matters was lost or overflowed
+  double q = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q = fma((double)v[e], (double)v[e], q);
+  return q;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_float(T v) { return static_cast<float>(v); }
+
+// One chunk [e0, e1) of a tensor: whole vectors of eight where the address is
+// 16-byte aligned, single elements before and after.
+template <typename T>
+__device__ __forceinline__ double sum_chunk(const void* gv, int64_t e0, int64_t e1) {
+  const T* g = static_cast<const T*>(gv);
+  const uintptr_t addr = reinterpret_cast<uintptr_t>(g + e0);
+  const int64_t head = min(e1, e0 + (int64_t)(((16 - (addr & 15)) & 15) / sizeof(T)));
+  const int64_t nv = (e1 - head) / 8;
+  double s = 0.0;
+  const int64_t singles = (head - e0) + (e1 - head - 8 * nv);
+  for (int64_t i = threadIdx.x; i < singles; i += blockDim.x) {
+    const double v = to_float(g[i < head - e0 ? e0 + i : head + 8 * nv + (i - (head - e0))]);
+    s = fma(v, v, s);
+  }
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < nv; i += blockDim.x) {
+    Vec8<T> r;
+    r.load(g + head + 8 * i);
+    float v[8];
+    r.unpack(v);
+    s += square8(v);
+  }
+  return s;
+}
+
+__device__ __forceinline__ double block_sum(double s) {
+  __shared__ double red[32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = (threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : 0.0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+__global__ void __launch_bounds__(256) grad_sum_kernel(const __grid_constant__ Table t, double* part) {
+  double s = 0.0;
+  const int chunks = t.chunk0[t.count];
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = find_tensor(t, c);
+    const int64_t e0 = (int64_t)(c - t.chunk0[i]) * kChunk;
+    const int64_t e1 = min(t.n[i], e0 + kChunk);
+    const int in = t.dtype[i] & 15;
+    if (in == MTGR_F32) s += sum_chunk<float>(t.g[i], e0, e1);
+    else if (in == MTGR_BF16) s += sum_chunk<__nv_bfloat16>(t.g[i], e0, e1);
+    else s += sum_chunk<__half>(t.g[i], e0, e1);
+  }
+  s = block_sum(s);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+
+template <typename T, typename O>
+__device__ __forceinline__ void scale_chunk(const void* gv, void* ov, int64_t e0, int64_t e1, float c) {
+  const T* g = static_cast<const T*>(gv);
+  O* o = static_cast<O*>(ov);
+  const uintptr_t ga = reinterpret_cast<uintptr_t>(g + e0), oa = reinterpret_cast<uintptr_t>(o + e0);
+  int64_t head = min(e1, e0 + (int64_t)(((16 - (ga & 15)) & 15) / sizeof(T)));
+  // vectors only where both sides are aligned from the same element on
+  const bool vec = ((oa + (uintptr_t)(head - e0) * sizeof(O)) & 15) == 0;
+  if (!vec) head = e1;
+  const int64_t nv = (e1 - head) / 8;
+  const int64_t singles = (head - e0) + (e1 - head - 8 * nv);
+  for (int64_t i = threadIdx.x; i < singles; i += blockDim.x) {
+    const int64_t e = i < head - e0 ? e0 + i : head + 8 * nv + (i - (head - e0));
+    o[e] = from_float<O>(to_float(g[e]) * c);
+  }
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < nv; i += blockDim.x) {
+    Vec8<T> r;
+    r.load(g + head + 8 * i);
+    float v[8];
+    r.unpack(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= c;
+    store8(o + head + 8 * i, v);
+  }
+}
+
+// parts: the sums of all launches of the first kernel. scale == 0: the norm only.
+__global__ void __launch_bounds__(256) grad_scale_kernel(const __grid_constant__ Table t, const double* part,
+                                                         int32_t parts, float max_norm, float inv_scale,
+                                                         int32_t scale, float* norm_out, int32_t* status) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < parts; i += blockDim.x) s += part[i];
+  s = block_sum(s);
+  const double norm = sqrt(s) * (double)inv_scale;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out != nullptr) {
+    *norm_out = (float)norm;
+    if (!isfinite(norm)) set_status(status, MTGR_ERR_RANGE);
+  }
+  if (scale == 0 || !isfinite(norm)) return;
+  const float ratio = (float)((double)max_norm / (norm + 1e-6));
+  const float c = inv_scale * fminf(1.0f, ratio);
+  const int chunks = t.chunk0[t.count];
+  // last chunks first: they are the ones L2 still holds
+  for (int k = chunks - 1 - (int)blockIdx.x; k >= 0; k -= gridDim.x) {
+    const int i = find_tensor(t, k);
+    const int64_t e0 = (int64_t)(k - t.chunk0[i]) * kChunk;
+    const int64_t e1 = min(t.n[i], e0 + kChunk);
+    if (c == 1.0f && t.g[i] == t.out[i]) continue;  // nothing to change in place
+    switch (t.dtype[i]) {
+      case MTGR_F32 | MTGR_F32 << 4: scale_chunk<float, float>(t.g[i], t.out[i], e0, e1, c); break;
+      case MTGR_BF16 | MTGR_BF16 << 4: scale_chunk<__nv_bfloat16, __nv_bfloat16>(t.g[i], t.out[i], e0, e1, c); break;
+      case MTGR_F16 | MTGR_F16 << 4: scale_chunk<__half, __half>(t.g[i], t.out[i], e0, e1, c); break;
+      case MTGR_BF16 | MTGR_F32 << 4: scale_chunk<__nv_bfloat16, float>(t.g[i], t.out[i], e0, e1, c); break;
+      default: scale_chunk<__half, float>(t.g[i], t.out[i], e0, e1, c); break;
+    }
+  }
+}
+
+// Blocks of a launch over `chunks` chunks.
+int grid_of(int64_t chunks) {
+  const int64_t most = (int64_t)device_sm_count() * 4;
+  return (int)(chunks < 1 ? 1 : (chunks < most ? chunks : most));
+}
+
+int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+
+// Tensors [first, last) of one launch as a table; empty tensors take no chunk.
+void fill(Table& t, const mtgr_grad_tensor* g, int first, int last) {
+  int64_t c = 0;
+  for (int i = first; i < last; ++i) {
+    t.g[i - first] = g[i].g;
+    t.out[i - first] = g[i].out;
+    t.n[i - first] = g[i].n;
+    t.dtype[i - first] = (uint8_t)(g[i].dtype | g[i].out_dtype << 4);
+    t.chunk0[i - first] = (int32_t)c;
+    c += chunks_of(g[i].n);
+  }
+  t.count = last - first;
+  t.chunk0[t.count] = (int32_t)c;
+}
+
+}  // namespace
+
+// The first kernel's blocks over all launches, 8 bytes each.
+size_t grad_clip_ws_bytes(const mtgr_grad_tensor* g, int32_t n) {
+  size_t parts = 0;
+  for (int32_t i = 0; i < n; i += kTable) {
+    int64_t c = 0;
+    for (int32_t k = i; k < n && k < i + kTable; ++k) c += chunks_of(g[k].n);
+    parts += (size_t)grid_of(c);
+  }
+  return align_up(parts * 8, 256);
+}
+
+// Kernels of a call, for the timer.
+int grad_clip_launches(const mtgr_grad_tensor* g, int32_t n) {
+  const int tables = (n + kTable - 1) / kTable;
+  for (int32_t i = 0; i < n; ++i)
+    if (g[i].out != nullptr) return 2 * tables;
+  return tables + 1;
+}
+
+int launch_grad_clip(const mtgr_grad_tensor* g, int32_t n, float max_norm, float inv_scale, float* norm,
+                     void* ws, int32_t* status, cudaStream_t s) {
+  double* part = static_cast<double*>(ws);
+  Table t;
+  t.count = 0;
+  t.chunk0[0] = 0;
+  int32_t parts = 0;
+  bool scale = false;
+  for (int32_t i = 0; i < n; i += kTable) {
+    fill(t, g, i, n < i + kTable ? n : i + kTable);
+    for (int k = 0; k < t.count; ++k) scale = scale || t.out[k] != nullptr;
+    const int grid = grid_of(t.chunk0[t.count]);
+    grad_sum_kernel<<<grid, 256, 0, s>>>(t, part + parts);
+    const int rc = launch_status();
+    if (rc != MTGR_OK) return rc;
+    parts += grid;
+  }
+  // the last table first, for what L2 holds; the norm is written once
+  const int32_t last = n > 0 ? (n - 1) / kTable * kTable : 0;
+  for (int32_t i = last; i >= 0; i -= kTable) {
+    if (n > kTable) fill(t, g, i, n < i + kTable ? n : i + kTable);
+    const int grid = scale ? grid_of(t.chunk0[t.count]) : 1;
+    grad_scale_kernel<<<grid, 256, 0, s>>>(t, part, parts, max_norm, inv_scale, scale ? 1 : 0,
+                                          i == last ? norm : nullptr, status);
+    const int rc = launch_status();
+    if (rc != MTGR_OK) return rc;
+    if (!scale) break;
+  }
+  return MTGR_OK;
+}
+
+}  // namespace mtgr

@@ -1,0 +1,60 @@
+// Arguments and launchers of the block-boundary, int8 and gradient-clipping
+// operators (boundary.cu, quant.cu, gemm_i8.cu, grad_clip.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/mtgr.h"
+
+namespace mtgr {
+
+constexpr int kMaxGroups = 32;  // the backward keeps the groups a team saw in 32 bits
+
+struct BoundaryFwdArgs {
+  int32_t T, d, G, gate;
+  float eps;
+  const int8_t* gid;
+  const void *o, *u, *x;
+  int64_t ld_o, ld_u;
+  const float *post_gamma, *post_beta, *scale, *pre_gamma, *pre_beta;
+  void *h, *y;
+  int32_t y_dtype;
+  float* y_scale;
+};
+
+struct BoundaryBwdArgs {
+  int32_t T, d, G, gate, o_dtype, dy_dtype;
+  float eps;
+  const int8_t* gid;
+  const void *o, *u, *x, *dh, *dy;
+  int64_t ld_o, ld_u, ld_do, ld_du;
+  const float *post_gamma, *post_beta, *scale, *pre_gamma, *pre_beta;
+  void *d_o, *du, *dx;
+  float *g_post_gamma, *g_post_beta, *g_scale, *g_pre_gamma, *g_pre_beta;
+  int32_t* status;
+  // filled by the launcher
+  int32_t teams, rows_per_team;
+  uint32_t* seen;
+  float* part;
+};
+
+int launch_boundary_fwd(const BoundaryFwdArgs& a, int32_t o_dtype, int32_t x_dtype, cudaStream_t s);
+size_t boundary_bwd_ws_bytes(int32_t T, int32_t d, int32_t G);
+int launch_boundary_bwd(BoundaryBwdArgs a, int32_t x_dtype, void* ws, cudaStream_t s);
+
+int launch_quantize_rows(int32_t M, int32_t K, int32_t x_dtype, const void* x, int64_t ld_x, int8_t* q,
+                         float* scale, cudaStream_t s);
+
+// out[m][n] = epi(sa[m] sb[n] sum_k a[m][k] b[n][k] + bias[n])
+int launch_gemm_i8(int M, int N, int K, const int8_t* a, const float* sa, const int8_t* b,
+                   const float* sb, const float* bias, int epi, const float* resid, int q_cols,
+                   int32_t out_dtype, void* out, int32_t* status, cudaStream_t s);
+
+size_t grad_clip_ws_bytes(const mtgr_grad_tensor* g, int32_t n);
+int grad_clip_launches(const mtgr_grad_tensor* g, int32_t n);
+int launch_grad_clip(const mtgr_grad_tensor* g, int32_t n, float max_norm, float inv_scale, float* norm,
+                     void* ws, int32_t* status, cudaStream_t s);
+
+}  // namespace mtgr

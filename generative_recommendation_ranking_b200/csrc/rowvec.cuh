@@ -1,0 +1,220 @@
+// Row vectors of eight elements for the row kernels (one row of [rows][d] per
+// team of threads): 16- or 32-byte loads and stores of fp32, bf16 and f16, sums
+// and maxima over a team, and the quantisation of a row to signed bytes.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace mtgr {
+
+// Eight consecutive elements as loaded, so that a thread's share of a row costs
+// as few registers as its bytes.
+template <typename T>
+struct Vec8;
+
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  }
+};
+
+template <>
+struct Vec8<__half> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __half* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+    }
+  }
+};
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  Vec8<float> r;
+  r.load(p);
+  r.unpack(v);
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------------ teams --
+// A row's threads: one warp (TEAM = 32), or a whole block (TEAM = blockDim.x,
+// a multiple of 32 up to 1024), whose warps meet in shared memory. Every
+// thread of the team gets the result, the same bits in each.
+template <int N, bool BLOCK>
+struct Team {
+  // one slot of partials per reduction in flight: two, used in turn, so that
+  // one barrier per reduction is enough
+  float (*part)[N][32];
+  int turn = 0;
+
+  __device__ __forceinline__ explicit Team(float (*p)[N][32]) : part(p) {}
+
+  __device__ __forceinline__ void sum(float (&v)[N]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if constexpr (BLOCK) {
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+      if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[turn][i][warp] = v[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float s = lane < nw ? part[turn][i][lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        v[i] = s;
+      }
+      turn ^= 1;
+    }
+  }
+  __device__ __forceinline__ float sum1(float a) {
+    float v[N] = {};
+    v[0] = a;
+    if constexpr (N == 1) {
+      sum(v);
+      return v[0];
+    } else {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+      if constexpr (BLOCK) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+        if (lane == 0) part[turn][0][warp] = a;
+        __syncthreads();
+        a = lane < nw ? part[turn][0][lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        turn ^= 1;
+      }
+      return a;
+    }
+  }
+  // maximum of non-negative values by their bits: a NaN is above every number
+  // and an infinity, so it is not lost
+  __device__ __forceinline__ uint32_t max_bits(uint32_t a) {
+    a = __reduce_max_sync(0xffffffffu, a);
+    if constexpr (BLOCK) {
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+      if (lane == 0) part[turn][0][warp] = __uint_as_float(a);
+      __syncthreads();
+      a = lane < nw ? __float_as_uint(part[turn][0][lane]) : 0u;
+      a = __reduce_max_sync(0xffffffffu, a);
+      turn ^= 1;
+    }
+    return a;
+  }
+};
+
+// -------------------------------------------------- rows in signed 8 bits --
+// A row's scale s = max(max |v|, 2^-100) * (1 / 127), 1 / 127 rounded to fp32, and
+// its values q = v / s rounded to the nearest integer, ties to even. 2^-100 keeps s and 1 / s normal numbers
+// for a row of zeros or of the smallest values, whose q are then 0. A row with
+// an infinity or a NaN gets s = NaN and q = 0, so that what reads it is NaN.
+struct RowScale {
+  float s, inv;
+};
+constexpr float kQuantTiny = 7.888609052210118e-31f;  // 2^-100
+
+__device__ __forceinline__ RowScale row_scale(uint32_t max_abs_bits) {
+  RowScale r;
+  if (max_abs_bits >= 0x7f800000u) {
+    r.s = __uint_as_float(0x7fc00000u);
+    r.inv = 0.f;
+  } else {
+    r.s = fmaxf(__uint_as_float(max_abs_bits), kQuantTiny) * (1.0f / 127.0f);
+    r.inv = 1.0f / r.s;
+  }
+  return r;
+}
+
+// Eight values to eight signed bytes. v * (1 / s) is off by up to two
+// roundings, which can put a value next to a border k + 1/2 on the wrong side;
+// the remainder v - q s is exact in fp32 (q has at most 7 bits and the
+// remainder is a multiple of an ulp of s or of v not above s/2 by more than a
+// few ulp), so it tells: beyond s / 2, or at s / 2 with an odd q, q moves by one.
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], const RowScale& r) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are the rounded integer
+  const float half = 0.5f * r.s;
+  uint32_t t[8];
+  float far = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float m = fmaf(v[e], r.inv, kMagic);
+    t[e] = __float_as_uint(m);
+    far = fmaxf(far, fabsf(fmaf(-(m - kMagic), r.s, v[e])));
+  }
+  if (far >= half) {  // rare; false for s = NaN
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float rem = fmaf(-(__uint_as_float(t[e]) - kMagic), r.s, v[e]);
+      const float ar = fabsf(rem);
+      if (ar > half || (ar == half && (t[e] & 1u))) t[e] += rem > 0.f ? 1u : 0xffffffffu;
+    }
+  }
+  if (r.inv == 0.f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = 0u;
+  }
+  uint2 o;
+  o.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+  o.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
+  return o;
+}
+
+}  // namespace mtgr

@@ -69,6 +69,7 @@ extern "C" {
 #define MTGR_F32 0
 #define MTGR_BF16 1
 #define MTGR_F16 2
+#define MTGR_I8 3                     /* signed bytes with a float scale per row (the int8 operators) */
 
 /* canonical mask-metadata tile (rows x columns of the user-relative grid) */
 #define MTGR_TILE_M 128
@@ -652,6 +653,154 @@ MTGR_API int mtgr_hstu_block_bwd(const mtgr_block_params* p, const mtgr_batch* b
                                  const float* d_x_in, const void* d_saved, const float* d_dy,
                                  float* d_dx, const mtgr_block_grads* grads, void* d_ws,
                                  size_t ws_bytes, mtgr_stream_t stream);
+
+/*
+ * The boundary between two blocks in one pass: the norm after a block, its gate,
+ * the residual scale and the norm before the next block (GroupLN: fun-rec 7.3.3,
+ * the GLN formula; gate and residual: summary page, Method, the block update
+ * equations). For every row i with group g = g(i):
+ *   n = GroupLN(o_i; post_gamma_g, post_beta_g)      (n = o_i without the post norm)
+ *   h = x_i + scale_g (.) n (.) f(u_i)               (scale 1 if NULL)
+ *   y = GroupLN(h; pre_gamma_g, pre_beta_g)          (no y without the pre norm)
+ * Statistics as in mtgr_group_layernorm (per token over d, biased variance),
+ * in fp32; y is taken from h before h is rounded to its type.
+ */
+#define MTGR_GATE_NONE 0    /* f = 1; u is not read */
+#define MTGR_GATE_LINEAR 1  /* f(u) = u */
+#define MTGR_GATE_SILU 2    /* f(u) = u / (1 + e^-u) */
+typedef struct mtgr_boundary_params {
+  int32_t d;                /* row length: a multiple of 8, at most 8192 */
+  int32_t G;                /* groups, at most 32 (a group id outside [0, G) counts as the nearest) */
+  float eps;
+  int32_t gate;             /* MTGR_GATE_* */
+  const float* post_gamma;  /* [G][d], or NULL together with post_beta: no post norm */
+  const float* post_beta;
+  const float* scale;       /* [G][d] or NULL */
+  const float* pre_gamma;   /* [G][d], or NULL together with pre_beta: no pre norm */
+  const float* pre_beta;
+} mtgr_boundary_params;
+
+/*
+ * Forward over T rows.
+ *   d_o [T][ld_o], d_u [T][ld_u] of o_dtype (MTGR_F32, MTGR_BF16, MTGR_F16); the
+ *     first d values of each row are read; ld a multiple of 8, at least d, so u
+ *     can be the U columns of a Q|K|V|U buffer
+ *   d_x, d_h [T][d] of x_dtype (MTGR_F32, MTGR_BF16); d_h may be d_x
+ *   d_y [T][d] of y_dtype: MTGR_F32, MTGR_BF16, or MTGR_I8 with d_y_scale [T], as
+ *     mtgr_quantize_rows would leave the fp32 y
+ * All pointers but d_group_id and d_y_scale 16-byte aligned. Timer class
+ * MTGR_TIMER_GLN.
+ */
+MTGR_API int mtgr_boundary_fwd(const mtgr_boundary_params* p, int32_t T, const int8_t* d_group_id,
+                               int32_t o_dtype, const void* d_o, int64_t ld_o, const void* d_u,
+                               int64_t ld_u, int32_t x_dtype, const void* d_x, void* d_h,
+                               int32_t y_dtype, void* d_y, float* d_y_scale, mtgr_stream_t stream);
+
+/* Parameter gradients of a boundary (device, fp32, [G][d], 16-byte aligned;
+ * written, not accumulated). Those of absent norms or scale are not read. */
+typedef struct mtgr_boundary_grads {
+  float* post_gamma;
+  float* post_beta;
+  float* scale;
+  float* pre_gamma;
+  float* pre_beta;
+} mtgr_boundary_grads;
+
+/*
+ * Backward: from dh = dL/dh through the stream (d_dh [T][d] of x_dtype; NULL: 0)
+ * and dy = dL/dy (d_dy [T][d] of dy_dtype, MTGR_F32 or MTGR_BF16; NULL without
+ * the pre norm) writes dx [T][d] (x_dtype; d_dx may be d_dh), do [T][ld_do] and,
+ * with a gate, du [T][ld_du] (o_dtype; values past d of a row are left as they
+ * are), and the parameter gradients, in the same order of sums in every run.
+ * d_o, d_u, d_x are the forward's inputs; without the pre norm d_x is not read.
+ * A do or du beyond f16 leaves MTGR_ERR_RANGE in d_status (may be NULL) and an
+ * infinity. Workspace: mtgr_boundary_bwd_workspace_bytes (0 on invalid
+ * parameters). Timer class MTGR_TIMER_BWD_GLN.
+ */
+MTGR_API size_t mtgr_boundary_bwd_workspace_bytes(int32_t T, const mtgr_boundary_params* p);
+MTGR_API int mtgr_boundary_bwd(const mtgr_boundary_params* p, int32_t T, const int8_t* d_group_id,
+                               int32_t o_dtype, const void* d_o, int64_t ld_o, const void* d_u,
+                               int64_t ld_u, int32_t x_dtype, const void* d_x, const void* d_dh,
+                               int32_t dy_dtype, const void* d_dy, void* d_do, int64_t ld_do,
+                               void* d_du, int64_t ld_du, void* d_dx,
+                               const mtgr_boundary_grads* grads, void* d_ws, size_t ws_bytes,
+                               int32_t* d_status, mtgr_stream_t stream);
+
+/*
+ * Rows to signed bytes with a scale each, for mtgr_gemm_i8 (activations by
+ * token, or a weight's rows by output channel):
+ *   scale_m = max(max_k |x_mk|, 2^-100) * (1 / 127) (1 / 127 rounded to fp32, the
+ *             product in fp32),
+ *   q_mk = x_mk / scale_m to the nearest integer, ties to even.
+ * A row that holds an infinity or a NaN gets scale NaN and q = 0.
+ *   d_x [M][ld_x] of x_dtype (MTGR_F32, MTGR_BF16, MTGR_F16), the first K values of
+ *     each row; K % 8 == 0, K <= 32768; ld_x a multiple of 8, at least K
+ *   d_q [M][K] int8, d_scale [M]; d_x, d_q 16-byte aligned
+ * Timer class MTGR_TIMER_ROWS.
+ */
+MTGR_API int mtgr_quantize_rows(int32_t M, int32_t K, int32_t x_dtype, const void* d_x, int64_t ld_x,
+                                int8_t* d_q, float* d_scale, mtgr_stream_t stream);
+
+/*
+ * Product of signed bytes with a scale per row of a (token) and of b (output
+ * channel), with mtgr_gemm's epilogues:
+ *   out[m][n] = epi( a_scale[m] b_scale[n] sum_k a[m][k] b[n][k] + bias[n] )
+ * The sums are exact (int32); scales, bias and epilogue in fp32, rounded once to
+ * out_dtype (MTGR_F32, MTGR_BF16, MTGR_F16; MTGR_EPI_RESID: MTGR_F32 only). An f16
+ * value beyond 65504 saturates and leaves MTGR_ERR_RANGE in d_status, as an
+ * internal wait that ran out leaves MTGR_ERR_TIMEOUT; with d_status NULL both go
+ * unseen. q_cols > 0 (a multiple of 32) halves columns [0, q_cols) at the end.
+ *   d_a [M][K], d_b [N][K] int8; d_out, d_resid [M][N], distinct buffers
+ *   K % 16 == 0, K < 131072, N % 8 == 0; d_a, d_b, d_b_scale, d_bias, d_resid,
+ *   d_out 16-byte aligned
+ * Runs on tcgen05. Timer class MTGR_TIMER_GEMM_QKVU, as mtgr_gemm.
+ */
+MTGR_API int mtgr_gemm_i8(int32_t M, int32_t N, int32_t K, const int8_t* d_a, const float* d_a_scale,
+                          const int8_t* d_b, const float* d_b_scale, const float* d_bias, int32_t epi,
+                          const float* d_resid, int32_t q_cols, int32_t out_dtype, void* d_out,
+                          int32_t* d_status, mtgr_stream_t stream);
+
+/*
+ * Linear layer with int8 weights: quantises the rows of x as mtgr_quantize_rows
+ * into the workspace (mtgr_linear_i8_workspace_bytes) and multiplies as
+ * mtgr_gemm_i8; the arguments and limits are theirs.
+ */
+MTGR_API size_t mtgr_linear_i8_workspace_bytes(int32_t M, int32_t K);
+MTGR_API int mtgr_linear_i8(int32_t M, int32_t N, int32_t K, int32_t x_dtype, const void* d_x,
+                            int64_t ld_x, const int8_t* d_w, const float* d_w_scale,
+                            const float* d_bias, int32_t epi, const float* d_resid, int32_t q_cols,
+                            int32_t out_dtype, void* d_out, void* d_ws, size_t ws_bytes,
+                            int32_t* d_status, mtgr_stream_t stream);
+
+/* One gradient of a set: n contiguous values at g (dtype MTGR_F32, MTGR_BF16 or
+ * MTGR_F16; any alignment of whole elements), clipped into out: of the same
+ * dtype, where out may be g, or MTGR_F32 elsewhere. out == NULL: only the norm. */
+typedef struct mtgr_grad_tensor {
+  const void* g;
+  void* out;
+  int64_t n;
+  int32_t dtype;
+  int32_t out_dtype;
+} mtgr_grad_tensor;
+
+/*
+ * Global 2-norm over n gradient tensors of a scaled loss, and clipping (the
+ * gradients mtgr_hstu_block_bwd and mtgr_boundary_bwd write; inv_scale = 1 / loss
+ * scale takes the scale out):
+ *   norm = inv_scale sqrt(sum of squares over all tensors)      -> d_norm [1] fp32
+ *   out = g inv_scale min(1, max_norm / (norm + 1e-6))
+ * h_grads is a HOST array, read before the call returns; the outputs must not
+ * overlap one another, nor a gradient other than their own. Outputs for all
+ * tensors, or NULL for all: the norm alone. Sums in fp64, in the same order in
+ * every run. A norm that is not finite leaves the outputs untouched and
+ * MTGR_ERR_RANGE in d_status (a step to skip). max_norm >= 0 (infinity: no
+ * clipping), inv_scale > 0 and finite. Workspace: mtgr_grad_clip_workspace_bytes
+ * (0 on invalid arguments). Timer class MTGR_TIMER_BWD_ROWS.
+ */
+MTGR_API size_t mtgr_grad_clip_workspace_bytes(const mtgr_grad_tensor* h_grads, int32_t n);
+MTGR_API int mtgr_grad_clip(const mtgr_grad_tensor* h_grads, int32_t n, float max_norm,
+                            float inv_scale, float* d_norm, void* d_ws, size_t ws_bytes,
+                            int32_t* d_status, mtgr_stream_t stream);
 
 /*
  * Self-test of the bounded waits (failure handling, not part of the method):

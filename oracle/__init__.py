@@ -47,3 +47,4 @@ from .tokens import (  # noqa: F401
     tokenize,
     candidate_heads,
 )
+from . import operators  # noqa: F401
