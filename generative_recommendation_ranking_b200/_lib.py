@@ -221,6 +221,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
+    if type(stream) is int:  # a cudaStream_t
+        return stream
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
@@ -229,6 +231,9 @@ def _stream(stream) -> int | None:
 def _check(fn: str, rc: int) -> None:
     if rc != MTGR_OK:
         raise MTGRError(fn, rc)
+
+
+check = _check
 
 
 def dtype_code(t: torch.dtype) -> int:

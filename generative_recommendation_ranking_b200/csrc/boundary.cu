@@ -207,28 +207,118 @@ int launch_fwd_t(const BoundaryFwdArgs& a, cudaStream_t s) {
 constexpr int kSlots = 5;
 enum { kPreGamma = 0, kPreBeta = 1, kScale = 2, kPostGamma = 3, kPostBeta = 4 };
 
-// A row's inputs as loaded.
+// A row's inputs wait in shared memory: each thread copies its own eight values of
+// every input up to two rows ahead (cp.async) and reads back only those, so no barrier
+// is needed, and the registers hold the sums instead. Stage layout: per thread
+// o, u (16 or 32 bytes), x, dh, dy; a thread's 16-byte pieces lie THREADS * 16
+// bytes apart, so that a warp's accesses fall in different banks.
+template <typename T>
+constexpr int kPieces = sizeof(T) / 2;  // 16-byte pieces of eight values: 1 or 2
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void copy8(uint32_t dst, uint32_t step, const T* src) {
+#pragma unroll
+  for (int i = 0; i < kPieces<T>; ++i) copy16(dst + i * step, reinterpret_cast<const char*>(src) + 16 * i);
+}
+__device__ __forceinline__ void unpack16(const uint4& a, float (&v)[8], __nv_bfloat16) {
+  Vec8<__nv_bfloat16> r;
+  r.a = a;
+  r.unpack(v);
+}
+__device__ __forceinline__ void unpack16(const uint4& a, float (&v)[8], __half) {
+  Vec8<__half> r;
+  r.a = a;
+  r.unpack(v);
+}
+template <typename T>
+__device__ __forceinline__ void read8(uint32_t src, uint32_t step, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const uint4 a = shared16(src), b = shared16(src + step);
+    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+    v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+  } else {
+    unpack16(shared16(src), v, T());
+  }
+}
+
+// Warps of a row's team.
+inline int bwd_warps(int d) {
+  const int w = (d + 255) / 256;
+  return w <= 4 ? w : (w <= 8 ? 8 : (w <= 16 ? 16 : 32));
+}
+
+// Rows in flight beside the one computed: two where 16 warps' stages fit in an SM.
+template <typename TO, int WARPS>
+constexpr int kAhead = WARPS == 32 ? 0 : (WARPS == 16 || sizeof(TO) == 4 ? 1 : 2);
+
 template <typename TO, typename TX>
-struct BwdRow {
-  Vec8<TO> o, u;
-  Vec8<TX> x, dh;
-  float4 dy[2];  // raw: two float4 of fp32, or the first one as eight bf16
-  int g;
+constexpr int kRowBytes = 16 * (2 * kPieces<TO> + 2 * kPieces<TX> + 2);
+
+// Sums over a team: a warp, or a block of WARPS warps that meet in shared memory
+// (partials in two slots used in turn, so that one barrier a sum is enough).
+template <int WARPS>
+struct Sums {
+  float2* part;  // [2][WARPS]
+  int turn = 0;
+  __device__ __forceinline__ float2 operator()(float a, float b) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    return meet(make_float2(a, b));
+  }
+  __device__ __forceinline__ float operator()(float a) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return meet(make_float2(a, 0.f)).x;
+  }
+  __device__ __forceinline__ float2 meet(float2 v) {
+    if constexpr (WARPS > 1) {
+      float2* p = part + turn * WARPS;
+      if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v;
+      __syncthreads();
+      v = p[0];
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) {
+        v.x += p[w].x;
+        v.y += p[w].y;
+      }
+      turn ^= 1;
+    }
+    return v;
+  }
 };
 
 // A team takes a contiguous run of rows (a user's segments are runs of one
 // group, so the group seldom changes), one vector of eight a thread: a warp for
-// d <= 256, several warps per block; above, a block of 32 ceil(d / 256) threads.
-// The next row's inputs are loaded before the current row is computed. The
-// parameter gradients gather in registers while the group stays the same; then
-// they go to the team's own slots of the workspace (each thread its own columns:
-// no atomics, and the same order of sums in every run).
-// MAXT: the largest block of the form (0: a warp per team, 4 warps a block).
-template <typename TO, typename TX, int MAXT>
-__global__ void __launch_bounds__(MAXT == 0 ? 128 : MAXT, 1) boundary_bwd_kernel(BoundaryBwdArgs a) {
-  constexpr bool BLOCK = MAXT != 0;
-  __shared__ float part[BLOCK ? 2 : 1][2][32];
-  Team<2, BLOCK> team(part);
+// d <= 256, four to a block; above, a block of WARPS = ceil(d / 256) warps (rounded
+// up to a power of two past four). The parameter gradients gather in registers
+// while the group stays the same; then they go to the team's own slots of the
+// workspace (each thread its own columns: no atomics, and the same order of sums
+// in every run).
+template <typename TO, typename TX, int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS <= 2 ? 8 / (WARPS == 1 ? 2 : 1) : (WARPS <= 16 ? 16 / WARPS : 1))
+    boundary_bwd_kernel(BoundaryBwdArgs a) {
+  constexpr int AHEAD = kAhead<TO, WARPS>;
+  extern __shared__ uint4 smem[];
+  __shared__ float2 part[2 * WARPS];
+  Sums<WARPS> sums{part};
+  constexpr bool BLOCK = WARPS > 1;
   const int tl = BLOCK ? threadIdx.x : threadIdx.x & 31;
   const int64_t ti = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (ti >= a.teams) return;
@@ -236,10 +326,14 @@ __global__ void __launch_bounds__(MAXT == 0 ? 128 : MAXT, 1) boundary_bwd_kernel
   const bool on = tl < (d >> 3);
   const int c0 = 8 * tl;
   const int64_t t0 = ti * a.rows_per_team;
-  const int64_t t1 = min((int64_t)a.T, t0 + a.rows_per_team);
-  const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr;
+  const int rows = (int)min((int64_t)a.rows_per_team, (int64_t)a.T - t0);
+  const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr, gate = a.gate != MTGR_GATE_NONE;
   const float inv_d = 1.0f / (float)d;
   float* slots = a.part + ti * a.G * kSlots * d + c0;
+  // this thread's pieces: stage s at base + s * stage, input pieces `step` apart
+  const uint32_t step = blockDim.x * 16, stage = kRowBytes<TO, TX> / 16 * step;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+  constexpr int PO = kPieces<TO>, PX = kPieces<TX>;
 
   float acc[kSlots][8];
 #pragma unroll
@@ -270,63 +364,56 @@ __global__ void __launch_bounds__(MAXT == 0 ? 128 : MAXT, 1) boundary_bwd_kernel
     }
     seen |= 1u << g_run;
   };
-  auto load_row = [&](int64_t t, BwdRow<TO, TX>& r) {
-    r.o.zero();
-    r.u.zero();
-    r.x.zero();
-    r.dh.zero();
-    r.dy[0] = r.dy[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    r.g = 0;
-    if (t >= t1) return;
-    r.g = clamp_group(a.gid, t, a.G);
-    if (!on) return;
-    r.o.load(static_cast<const TO*>(a.o) + t * a.ld_o + c0);
-    if (a.gate != MTGR_GATE_NONE) r.u.load(static_cast<const TO*>(a.u) + t * a.ld_u + c0);
-    if (pre) {
-      r.x.load(static_cast<const TX*>(a.x) + t * d + c0);
-      if (a.dy_dtype == MTGR_F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.dy) + t * d + c0);
-        r.dy[0] = p[0];
-        r.dy[1] = p[1];
-      } else {
-        r.dy[0] = *reinterpret_cast<const float4*>(static_cast<const __nv_bfloat16*>(a.dy) + t * d + c0);
+  auto copy_row = [&](int r, int s) {
+    if (on && r < rows) {
+      const int64_t t = t0 + r;
+      const uint32_t at = base + s * stage;
+      copy8(at, step, static_cast<const TO*>(a.o) + t * a.ld_o + c0);
+      if (gate) copy8(at + PO * step, step, static_cast<const TO*>(a.u) + t * a.ld_u + c0);
+      if (a.dh != nullptr) copy8(at + (2 * PO + PX) * step, step, static_cast<const TX*>(a.dh) + t * d + c0);
+      if (pre) {
+        copy8(at + 2 * PO * step, step, static_cast<const TX*>(a.x) + t * d + c0);
+        if (a.dy_dtype == MTGR_F32)
+          copy8(at + (2 * PO + 2 * PX) * step, step, static_cast<const float*>(a.dy) + t * d + c0);
+        else
+          copy8(at + (2 * PO + 2 * PX) * step, step, static_cast<const __nv_bfloat16*>(a.dy) + t * d + c0);
       }
     }
-    if (a.dh != nullptr) r.dh.load(static_cast<const TX*>(a.dh) + t * d + c0);
+    copy_commit();
   };
 
-  BwdRow<TO, TX> cur;
-  load_row(t0, cur);
-  for (int64_t t = t0; t < t1; ++t) {
-    BwdRow<TO, TX> nxt;
-    load_row(t + 1, nxt);
-    if (cur.g != g_run) {
-      flush();
-      g_run = cur.g;
-    }
-    const int64_t pc = (int64_t)cur.g * d + c0;
-    // n and f again
-    float oh[8], n[8], f[8], uv[8], gp[8], sc[8];
-    float rstd_o = 1.f;
-    cur.o.unpack(oh);
-    if (post) {
-      float s = 0.f, q = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += oh[e];
-      const float mean = team.sum1(s) * inv_d;
+  for (int r = 0; r < AHEAD; ++r) copy_row(r, r);
+  int g = rows > 0 ? clamp_group(a.gid, t0, a.G) : 0, s = 0;
+  for (int r = 0; r < rows; ++r) {
+    copy_row(r + AHEAD, s == 0 ? AHEAD : s - 1);  // stage (s + AHEAD) mod (AHEAD + 1)
+    const int g_next = r + 1 < rows ? clamp_group(a.gid, t0 + r + 1, a.G) : 0;
+    copy_wait<AHEAD>();
+    const uint32_t at = base + s * stage;
+    if (g != g_run) {
+      flush();
+      g_run = g;
+    }
+    const int64_t t = t0 + r, pc = (int64_t)g * d + c0;
+    // n and f again (what is past d is 0, so that it adds nothing to a sum)
+    float oh[8] = {}, n[8], f[8], gp[8] = {}, sc[8];
+    float rstd_o = 1.f;
+    if (on) read8<TO>(at, step, oh);
+    if (post) {
+      float q = 0.f, m = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m += oh[e];
+      m = sums(m) * inv_d;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        oh[e] = on ? oh[e] - mean : 0.f;
+        oh[e] = on ? oh[e] - m : 0.f;
         q = fmaf(oh[e], oh[e], q);
       }
-      rstd_o = 1.0f / sqrtf(team.sum1(q) * inv_d + a.eps);
-      float bt[8];
+      rstd_o = 1.0f / sqrtf(sums(q) * inv_d + a.eps);
+      float bt[8] = {};
       if (on) {
         load8(a.post_gamma + pc, gp);
         load8(a.post_beta + pc, bt);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) gp[e] = bt[e] = 0.f;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -337,107 +424,98 @@ __global__ void __launch_bounds__(MAXT == 0 ? 128 : MAXT, 1) boundary_bwd_kernel
 #pragma unroll
       for (int e = 0; e < 8; ++e) n[e] = oh[e];
     }
-    cur.u.unpack(uv);
-    if (a.gate != MTGR_GATE_NONE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 1.f;
+    if (gate) {
+      float uv[8] = {};
+      if (on) read8<TO>(at + PO * step, step, uv);
       gate8(a.gate, uv, f);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 1.f;
     }
-    if (a.scale != nullptr && on) {
-      load8(a.scale + pc, sc);
-    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sc[e] = 1.f;
-    }
+    for (int e = 0; e < 8; ++e) sc[e] = 1.f;
+    if (a.scale != nullptr && on) load8(a.scale + pc, sc);
     // H: the gradient at h
-    float H[8];
-    cur.dh.unpack(H);
+    float H[8] = {};
     if (pre) {
-      float hh[8], s = 0.f, q = 0.f;
-      cur.x.unpack(hh);
+      float hh[8] = {}, m = 0.f, q = 0.f;
+      if (on) read8<TX>(at + 2 * PO * step, step, hh);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         hh[e] = fmaf(n[e] * f[e], sc[e], hh[e]);
-        s += hh[e];
+        m += hh[e];
       }
-      const float mean = team.sum1(on ? s : 0.f) * inv_d;
+      m = sums(on ? m : 0.f) * inv_d;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        hh[e] = on ? hh[e] - mean : 0.f;
+        hh[e] = on ? hh[e] - m : 0.f;
         q = fmaf(hh[e], hh[e], q);
       }
-      const float rstd_h = 1.0f / sqrtf(team.sum1(q) * inv_d + a.eps);
-      float dy[8], gm[8];
-      if (a.dy_dtype == MTGR_F32) {
-        const float4 p0 = cur.dy[0], p1 = cur.dy[1];
-        dy[0] = p0.x; dy[1] = p0.y; dy[2] = p0.z; dy[3] = p0.w;
-        dy[4] = p1.x; dy[5] = p1.y; dy[6] = p1.z; dy[7] = p1.w;
-      } else {
-        const float w[4] = {cur.dy[0].x, cur.dy[0].y, cur.dy[0].z, cur.dy[0].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          dy[2 * k] = __uint_as_float(__float_as_uint(w[k]) << 16);
-          dy[2 * k + 1] = __uint_as_float(__float_as_uint(w[k]) & 0xffff0000u);
-        }
-      }
+      const float rstd_h = 1.0f / sqrtf(sums(q) * inv_d + a.eps);
+      float dy[8] = {}, gm[8] = {};
       if (on) {
+        if (a.dy_dtype == MTGR_F32) read8<float>(at + (2 * PO + 2 * PX) * step, step, dy);
+        else read8<__nv_bfloat16>(at + (2 * PO + 2 * PX) * step, step, dy);
         load8(a.pre_gamma + pc, gm);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) gm[e] = 0.f;
       }
-      float m[2] = {0.f, 0.f};
+      float m0 = 0.f, m1 = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         hh[e] *= rstd_h;
         acc[kPreGamma][e] = fmaf(dy[e], hh[e], acc[kPreGamma][e]);
         acc[kPreBeta][e] += dy[e];
         dy[e] *= gm[e];
-        m[0] += dy[e];
-        m[1] = fmaf(dy[e], hh[e], m[1]);
+        m0 += dy[e];
+        m1 = fmaf(dy[e], hh[e], m1);
       }
-      team.sum(m);
-      const float m0 = m[0] * inv_d, m1 = m[1] * inv_d;
+      const float2 ms = sums(m0, m1);
+      m0 = ms.x * inv_d;
+      m1 = ms.y * inv_d;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) H[e] = fmaf(rstd_h, dy[e] - m0 - hh[e] * m1, H[e]);
+      for (int e = 0; e < 8; ++e) H[e] = rstd_h * (dy[e] - m0 - hh[e] * m1);
+    }
+    if (a.dh != nullptr && on) {
+      float dh[8];
+      read8<TX>(at + (2 * PO + PX) * step, step, dh);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) H[e] += dh[e];
     }
     if (on) store8(static_cast<TX*>(a.dx) + t * d + c0, H);
-    float b[8], m[2] = {0.f, 0.f};
-    {
+    float b[8], m0 = 0.f, m1 = 0.f;
+    if (gate) {
       float du[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float p = H[e] * sc[e];
-        acc[kScale][e] = fmaf(H[e], n[e] * f[e], acc[kScale][e]);
-        b[e] = p * f[e];  // dn
-        du[e] = p * n[e];
-        acc[kPostGamma][e] = fmaf(b[e], oh[e], acc[kPostGamma][e]);
-        acc[kPostBeta][e] += b[e];
-      }
-      if (a.gate == MTGR_GATE_SILU) {
+      for (int e = 0; e < 8; ++e) du[e] = H[e] * sc[e] * n[e];
+      if (a.gate == MTGR_GATE_SILU && on) {
+        float uv[8];
+        read8<TO>(at + PO * step, step, uv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float sg = sigmoid_f32(uv[e]);
           du[e] *= fmaf(f[e], 1.0f - sg, sg);  // sigmoid(u) (1 + u (1 - sigmoid(u)))
         }
       }
-      if (a.gate != MTGR_GATE_NONE && on) {
+      if (on) {
         store8(static_cast<TO*>(a.du) + t * a.ld_du + c0, du);
         if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16)
 #pragma unroll
           for (int e = 0; e < 8; ++e) range_bad |= fabsf(du[e]) > 65504.f;
       }
     }
-    if (post) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        b[e] *= gp[e];
-        m[0] += b[e];
-        m[1] = fmaf(b[e], oh[e], m[1]);
-      }
-      team.sum(m);
-      const float m0 = m[0] * inv_d, m1 = m[1] * inv_d;
+    for (int e = 0; e < 8; ++e) {
+      const float hf = H[e] * f[e];
+      acc[kScale][e] = fmaf(hf, n[e], acc[kScale][e]);
+      b[e] = hf * sc[e];  // dn
+      acc[kPostGamma][e] = fmaf(b[e], oh[e], acc[kPostGamma][e]);
+      acc[kPostBeta][e] += b[e];
+      b[e] = post ? b[e] * gp[e] : b[e];
+      m0 += b[e];
+      m1 = fmaf(b[e], oh[e], m1);
+    }
+    if (post) {
+      const float2 ms = sums(m0, m1);
+      m0 = ms.x * inv_d;
+      m1 = ms.y * inv_d;
 #pragma unroll
       for (int e = 0; e < 8; ++e) b[e] = rstd_o * (b[e] - m0 - oh[e] * m1);
     }
@@ -447,7 +525,8 @@ __global__ void __launch_bounds__(MAXT == 0 ? 128 : MAXT, 1) boundary_bwd_kernel
 #pragma unroll
         for (int e = 0; e < 8; ++e) range_bad |= fabsf(b[e]) > 65504.f;
     }
-    cur = nxt;
+    g = g_next;
+    s = s == AHEAD ? 0 : s + 1;
   }
   flush();
   if (tl == 0) a.seen[ti] = seen;
@@ -492,18 +571,31 @@ __global__ void __launch_bounds__(512) boundary_bwd_reduce_kernel(BoundaryBwdArg
       make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
 }
 
+template <typename TO, typename TX, int WARPS>
+int launch_bwd_w(const BoundaryBwdArgs& a, cudaStream_t s) {
+  const int threads = WARPS == 1 ? 128 : 32 * WARPS;
+  const int bytes = threads * (kAhead<TO, WARPS> + 1) * kRowBytes<TO, TX>;
+  auto kern = boundary_bwd_kernel<TO, TX, WARPS>;
+  if (bytes > 40 * 1024 &&  // 48 KB without asking, some of it static
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return MTGR_ERR_CUDA;
+  kern<<<WARPS == 1 ? (a.teams + 3) / 4 : a.teams, threads, bytes, s>>>(a);
+  return launch_status();
+}
+
 template <typename TO, typename TX>
 int launch_bwd_t(const BoundaryBwdArgs& a, cudaStream_t s) {
   if (a.teams > 0) {
-    const int threads = 32 * ((a.d + 255) / 256);
-    if (a.d <= 256) {
-      boundary_bwd_kernel<TO, TX, 0><<<(a.teams + 3) / 4, 128, 0, s>>>(a);
-    } else if (a.d <= 2048) {
-      boundary_bwd_kernel<TO, TX, 256><<<a.teams, threads, 0, s>>>(a);
-    } else {
-      boundary_bwd_kernel<TO, TX, 1024><<<a.teams, threads, 0, s>>>(a);
+    int rc = MTGR_OK;
+    switch (bwd_warps(a.d)) {
+      case 1: rc = launch_bwd_w<TO, TX, 1>(a, s); break;
+      case 2: rc = launch_bwd_w<TO, TX, 2>(a, s); break;
+      case 3: rc = launch_bwd_w<TO, TX, 3>(a, s); break;
+      case 4: rc = launch_bwd_w<TO, TX, 4>(a, s); break;
+      case 8: rc = launch_bwd_w<TO, TX, 8>(a, s); break;
+      case 16: rc = launch_bwd_w<TO, TX, 16>(a, s); break;
+      default: rc = launch_bwd_w<TO, TX, 32>(a, s); break;
     }
-    const int rc = launch_status();
     if (rc != MTGR_OK) return rc;
   }
   const int64_t n = (int64_t)a.G * kSlots * a.d;
@@ -513,11 +605,11 @@ int launch_bwd_t(const BoundaryBwdArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Teams of the backward: as many as are resident at once (register-bound: 16
-// warps an SM), at least 4 rows each, and at most 256 MB of gradient slots.
+// Teams of the backward: as many as are resident at once (16 warps an SM, by
+// registers), at least 4 rows each, and at most 256 MB of gradient slots.
 int32_t boundary_bwd_teams(int32_t T, int32_t d, int32_t G) {
   if (T <= 0) return 0;
-  const int warps = (d + 255) / 256;
+  const int warps = bwd_warps(d);
   int64_t teams = (int64_t)device_sm_count() * (16 / warps > 0 ? 16 / warps : 1);
   const int64_t slot_bytes = (int64_t)G * kSlots * d * 4;
   const int64_t most = (256ll << 20) / slot_bytes;

@@ -8,6 +8,9 @@ tied to ``stream``, so it may be dropped while the work still runs.
 
 from __future__ import annotations
 
+import functools
+from ctypes import byref as _byref
+
 import torch
 
 from . import _lib
@@ -21,94 +24,106 @@ _FLOATS = (torch.float32, torch.bfloat16, torch.float16)
 _STREAM_TYPES = (torch.float32, torch.bfloat16)
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+_device_now = torch._C._cuda_getDevice
+_stream_now = torch._C._cuda_getCurrentRawStream
 
 
-class _On:
-    """The device of a call's tensors, made the current one for the call (the
-    library works on the current device), and its stream."""
+def _on_its_device(fn):
+    """Runs ``fn`` with its first tensor's device as the current one (the library
+    works on the current device)."""
 
-    __slots__ = ("index", "guard", "stream", "other")
+    first = fn.__code__.co_varnames[0]
 
-    def __init__(self, t: torch.Tensor, stream):
-        _need(t.is_cuda, "a device tensor is needed")
-        self.index = t.device.index
-        self.guard = None if self.index == torch.cuda.current_device() else torch.cuda.device(self.index)
-        current = torch.cuda.current_stream(self.index)
-        self.stream = current if stream is None else stream
-        self.other = stream is not None and stream != current
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        t = args[0] if args else kwargs.get(first)
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{first}: a device tensor is needed")
+        if t.get_device() == _device_now():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(t.device):
+            return fn(*args, **kwargs)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
-
-    def empty(self, shape, dtype) -> torch.Tensor:
-        t = torch.empty(shape, dtype=dtype, device=self.index)
-        if self.other:
-            t.record_stream(self.stream)
-        return t
-
-    def bytes(self, n: int) -> torch.Tensor:
-        return self.empty(max(int(n), 256), torch.uint8)
-
-    def given(self, name, t, shape, dtypes, rows=False) -> None:
-        """Checks one tensor; ``rows``: rows may be further apart than their length."""
-        if t.shape != shape or t.dtype not in dtypes or t.device.index != self.index or not t.is_cuda:
-            raise ValueError(f"{name}: {tuple(shape)} of {' / '.join(map(str, dtypes))} on cuda:{self.index} "
-                             f"is needed, got {tuple(t.shape)} of {t.dtype} on {t.device}")
-        if rows:
-            if t.shape[0] and (t.stride(1) != 1 and t.shape[1] > 1 or t.shape[0] > 1 and
-                               (t.stride(0) < t.shape[1] or t.stride(0) % 8)):
-                raise ValueError(f"{name}: rows of consecutive values, a multiple of 8 apart, are needed")
-        elif not t.is_contiguous():
-            raise ValueError(f"{name}: a contiguous tensor is needed")
+    return call
 
 
-_F32 = (torch.float32,)
+def _where(stream, dev: int):
+    """(cudaStream_t, the stream if it is not the current one) of a call."""
+    now = _stream_now(dev)
+    if stream is None or stream.cuda_stream == now:
+        return now, None
+    return stream.cuda_stream, stream
 
 
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """``t`` with a row stride that the library accepts: that of a single row means nothing."""
-    if t.shape[0] <= 1 and (t.stride(0) < t.shape[1] or t.stride(0) % 8):
-        return t.as_strided(t.shape, (t.shape[1], 1))
+def _new(shape, dtype, dev: int, other) -> torch.Tensor:
+    """A buffer for the call's stream: the allocator counts it to the current
+    stream, so one on another stream is recorded there."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if other is not None:
+        t.record_stream(other)
     return t
 
 
-def _boundary(on, x, o, u, group_id, post_gamma, post_beta, scale, pre_gamma, pre_beta, eps, gate):
-    """Checks what the forward and the backward share; returns the parameters and u."""
-    _need(gate in GATES, f"gate {gate!r}: one of none, linear, silu")
-    _need(x.dim() == 2, "x: [T, d] is needed")
+def _given(name: str, t, shape, dtype, dev: int) -> None:
+    if not (t.shape == shape and t.dtype == dtype and t.get_device() == dev and t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous {tuple(shape)} of {dtype} on cuda:{dev} is needed, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}, strides {t.stride()}")
+
+
+def _given_rows(name: str, t, shape, dtypes, dev: int) -> int:
+    """Checks a tensor whose rows may be further apart than their length; returns
+    how far (that of a single row means nothing)."""
+    if t.shape == shape and t.dtype in dtypes and t.get_device() == dev:
+        ld, one = t.stride()
+        rows, n = shape
+        if rows <= 1:
+            ld = n
+        if (one == 1 or n <= 1 or rows == 0) and ld >= n and ld % 8 == 0:
+            return ld
+    raise ValueError(f"{name}: {tuple(shape)} of {' / '.join(map(str, dtypes))} on cuda:{dev}, rows of consecutive "
+                     f"values a multiple of 8 apart, is needed, got {tuple(t.shape)} of {t.dtype} on {t.device}, "
+                     f"strides {t.stride()}")
+
+
+_PARAMS = ("post_gamma", "post_beta", "scale", "pre_gamma", "pre_beta")
+_CODE = {torch.float32: _lib.MTGR_F32, torch.bfloat16: _lib.MTGR_BF16, torch.float16: _lib.MTGR_F16,
+         torch.int8: _lib.MTGR_I8}
+
+
+def _boundary(x, o, u, group_id, values, eps, gate, dev):
+    """Checks what the forward and the backward share: (parameters, row strides of o and u)."""
+    if gate not in GATES:
+        raise ValueError(f"gate {gate!r}: one of none, linear, silu")
+    if x.dim() != 2 or x.dtype not in _STREAM_TYPES or not x.is_contiguous():
+        raise ValueError(f"x: a contiguous [T, d] of float32 or bfloat16 is needed, got {tuple(x.shape)} of {x.dtype}")
     shape = x.shape
     T, d = shape
-    on.given("x", x, shape, _STREAM_TYPES)
-    on.given("o", o, shape, _FLOATS, rows=True)
-    on.given("group_id", group_id, (T,), (torch.int8,))
+    ld_o = _given_rows("o", o, shape, _FLOATS, dev)
+    _given("group_id", group_id, shape[:1], torch.int8, dev)
     code = GATES[gate]
-    if code == MTGR_GATE_NONE:
-        u = None
-    else:
-        _need(u is not None, "u is needed with a gate")
-        on.given("u", u, shape, (o.dtype,), rows=True)
-        u = _rows(u)
-    _need((post_gamma is None) == (post_beta is None), "post_gamma and post_beta come together")
-    _need((pre_gamma is None) == (pre_beta is None), "pre_gamma and pre_beta come together")
-    G = next((p.shape[0] for p in (post_gamma, pre_gamma, scale) if p is not None), 1)
-    ptr = [None] * 5
-    for i, (name, p) in enumerate((("post_gamma", post_gamma), ("post_beta", post_beta), ("scale", scale),
-                                   ("pre_gamma", pre_gamma), ("pre_beta", pre_beta))):
+    ld_u = 0
+    if code != MTGR_GATE_NONE:
+        if u is None:
+            raise ValueError("u is needed with a gate")
+        ld_u = _given_rows("u", u, shape, (o.dtype,), dev)
+    if (values[0] is None) != (values[1] is None) or (values[3] is None) != (values[4] is None):
+        raise ValueError("a norm's gamma and beta come together")
+    G = 1
+    for p in values:
         if p is not None:
-            on.given(name, p, (G, d), _F32)
-            ptr[i] = p.data_ptr()
-    return MtgrBoundaryParams(d, G, eps, code, *ptr), _rows(o), u
+            G = p.shape[0]
+            break
+    ptr = []
+    for name, p in zip(_PARAMS, values):
+        if p is None:
+            ptr.append(None)
+        else:
+            _given(name, p, (G, d), torch.float32, dev)
+            ptr.append(p.data_ptr())
+    return MtgrBoundaryParams(d, G, eps, code, *ptr), ld_o, ld_u
 
 
+@_on_its_device
 def boundary_forward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=None, pre_gamma=None,
                      pre_beta=None, *, gate="linear", y_dtype=torch.bfloat16, eps: float = EPS, h=None,
                      y=None, y_scale=None, stream=None):
@@ -125,32 +140,37 @@ def boundary_forward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=N
     with a scale, for gemm_i8). Returns (h, y, y_scale); y is None without the
     pre norm, y_scale but for int8. ``h`` may be given as ``x``: in place.
     """
-    with _On(x, stream) as on:
-        p, o, u = _boundary(on, x, o, u, group_id, post_gamma, post_beta, scale, pre_gamma, pre_beta, eps, gate)
-        T, d = x.shape
-        if h is None:
-            h = on.empty(x.shape, x.dtype)
+    dev = x.get_device()
+    raw, other = _where(stream, dev)
+    p, ld_o, ld_u = _boundary(x, o, u, group_id, (post_gamma, post_beta, scale, pre_gamma, pre_beta), eps, gate, dev)
+    shape = x.shape
+    if h is None:
+        h = _new(shape, x.dtype, dev, other)
+    else:
+        _given("h", h, shape, x.dtype, dev)
+    if pre_gamma is None:
+        y = y_scale = None
+    else:
+        if y_dtype not in (torch.float32, torch.bfloat16, torch.int8):
+            raise ValueError(f"y_dtype {y_dtype}: float32, bfloat16 or int8")
+        if y is None:
+            y = _new(shape, y_dtype, dev, other)
         else:
-            on.given("h", h, x.shape, (x.dtype,))
-        if pre_gamma is None:
-            y = y_scale = None
+            _given("y", y, shape, y_dtype, dev)
+        if y_dtype != torch.int8:
+            y_scale = None
+        elif y_scale is None:
+            y_scale = _new(shape[:1], torch.float32, dev, other)
         else:
-            _need(y_dtype in (torch.float32, torch.bfloat16, torch.int8),
-                  f"y_dtype {y_dtype}: float32, bfloat16 or int8")
-            if y is None:
-                y = on.empty(x.shape, y_dtype)
-            else:
-                on.given("y", y, x.shape, (y_dtype,))
-            if y_dtype != torch.int8:
-                y_scale = None
-            elif y_scale is None:
-                y_scale = on.empty((T,), torch.float32)
-            else:
-                on.given("y_scale", y_scale, (T,), _F32)
-        _lib.mtgr_boundary_fwd(p, T, group_id, o, u, x, h, y, y_scale, on.stream)
+            _given("y_scale", y_scale, shape[:1], torch.float32, dev)
+    _lib.check("mtgr_boundary_fwd", _lib.load().mtgr_boundary_fwd(
+        _byref(p), shape[0], group_id.data_ptr(), _CODE[o.dtype], o.data_ptr(), ld_o, u.data_ptr() if ld_u else None,
+        ld_u, _CODE[x.dtype], x.data_ptr(), h.data_ptr(), 0 if y is None else _CODE[y_dtype],
+        None if y is None else y.data_ptr(), None if y_scale is None else y_scale.data_ptr(), raw))
     return h, y, y_scale
 
 
+@_on_its_device
 def boundary_backward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=None, pre_gamma=None,
                       pre_beta=None, dh=None, dy=None, *, gate="linear", eps: float = EPS, ws=None,
                       status=None, stream=None) -> dict:
@@ -158,55 +178,80 @@ def boundary_backward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=
     through the stream (None: 0; [T, d] of x's type) and ``dy`` = dL/dy ([T, d],
     float32 or bfloat16; None without the pre norm). Returns a dict: ``dx``,
     ``do``, ``du`` (with a gate) in the types of x, o, u, and the float32
-    gradients of the parameters that were given, under their names.
+    gradients of the parameters that were given, under their names. ``status``: a
+    device int32 word (zeroed by the caller) that tells of f16 gradients out of range.
     """
-    with _On(x, stream) as on:
-        p, o, u = _boundary(on, x, o, u, group_id, post_gamma, post_beta, scale, pre_gamma, pre_beta, eps, gate)
-        T, d = x.shape
-        if dh is not None:
-            on.given("dh", dh, x.shape, (x.dtype,))
-        if pre_gamma is not None:
-            _need(dy is not None, "dy is needed with the pre norm")
-            on.given("dy", dy, x.shape, _STREAM_TYPES)
-        else:
-            _need(dh is not None and dy is None, "without the pre norm dh is needed, and no dy")
-        out = dict(dx=on.empty(x.shape, x.dtype), do=on.empty(x.shape, o.dtype))
-        if u is not None:
-            out["du"] = on.empty(x.shape, o.dtype)
-        # one allocation for the parameters' gradients
-        names = [n for n, t in (("post_gamma", post_gamma), ("post_beta", post_beta), ("scale", scale),
-                                ("pre_gamma", pre_gamma), ("pre_beta", pre_beta)) if t is not None]
-        flat = on.empty((len(names), p.G, d), torch.float32)
+    dev = x.get_device()
+    raw, other = _where(stream, dev)
+    values = (post_gamma, post_beta, scale, pre_gamma, pre_beta)
+    p, ld_o, ld_u = _boundary(x, o, u, group_id, values, eps, gate, dev)
+    shape = x.shape
+    T, d = shape
+    if dh is not None:
+        _given("dh", dh, shape, x.dtype, dev)
+    if pre_gamma is not None:
+        if dy is None or dy.dtype not in _STREAM_TYPES:
+            raise ValueError("dy of float32 or bfloat16 is needed with the pre norm")
+        _given("dy", dy, shape, dy.dtype, dev)
+    elif dh is None or dy is not None:
+        raise ValueError("without the pre norm dh is needed, and no dy")
+    if status is not None:
+        _given("status", status, (1,), torch.int32, dev)
+    dx, do = _new(shape, x.dtype, dev, other), _new(shape, o.dtype, dev, other)
+    out = dict(dx=dx, do=do)
+    du = None
+    if ld_u:
+        du = out["du"] = _new(shape, o.dtype, dev, other)
+    # one allocation for the parameters' gradients
+    names = [n for n, v in zip(_PARAMS, values) if v is not None]
+    ptr = [None] * 5
+    if names:
+        flat = _new((len(names), p.G, d), torch.float32, dev, other)
         out.update(zip(names, flat.unbind(0)))
-        g = MtgrBoundaryGrads(*[out[n].data_ptr() if n in out else None
-                                for n in ("post_gamma", "post_beta", "scale", "pre_gamma", "pre_beta")])
-        need = _lib.mtgr_boundary_bwd_workspace_bytes(T, p)
-        if ws is None or ws.numel() < need:
-            ws = on.bytes(need)
-        _lib.mtgr_boundary_bwd(p, T, group_id, o, u, x, dh, dy, out["do"], out.get("du"), out["dx"], g, ws,
-                               status, on.stream)
+        base, k = flat.data_ptr(), 0
+        for i, v in enumerate(values):
+            if v is not None:
+                ptr[i] = base + 4 * k * p.G * d
+                k += 1
+    need = _lib.load().mtgr_boundary_bwd_workspace_bytes(T, _byref(p))
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws, room = _new((max(need, 256),), torch.uint8, dev, other), max(need, 256)
+    else:
+        room = ws.numel() * ws.element_size()
+    _lib.check("mtgr_boundary_bwd", _lib.load().mtgr_boundary_bwd(
+        _byref(p), T, group_id.data_ptr(), _CODE[o.dtype], o.data_ptr(), ld_o, u.data_ptr() if ld_u else None, ld_u,
+        _CODE[x.dtype], x.data_ptr(), None if dh is None else dh.data_ptr(), 0 if dy is None else _CODE[dy.dtype],
+        None if dy is None else dy.data_ptr(), do.data_ptr(), d, None if du is None else du.data_ptr(), d,
+        dx.data_ptr(), _byref(MtgrBoundaryGrads(*ptr)), ws.data_ptr(), room,
+        None if status is None else status.data_ptr(), raw))
     return out
 
 
+@_on_its_device
 def quantize_rows(x, q=None, scale=None, stream=None):
     """Rows of ``x`` [M, K] (float32, bfloat16, float16) to signed bytes with a
     float32 scale each (mtgr_quantize_rows): returns (q [M, K] int8, scale [M]).
     A weight's rows give the scales of its output channels."""
-    with _On(x, stream) as on:
-        _need(x.dim() == 2, "x: [M, K] is needed")
-        on.given("x", x, x.shape, _FLOATS, rows=True)
-        if q is None:
-            q = on.empty(x.shape, torch.int8)
-        else:
-            on.given("q", q, x.shape, (torch.int8,))
-        if scale is None:
-            scale = on.empty(x.shape[:1], torch.float32)
-        else:
-            on.given("scale", scale, x.shape[:1], _F32)
-        _lib.mtgr_quantize_rows(_rows(x), q, scale, on.stream)
+    dev = x.get_device()
+    raw, other = _where(stream, dev)
+    if x.dim() != 2:
+        raise ValueError("x: [M, K] is needed")
+    shape = x.shape
+    ld = _given_rows("x", x, shape, _FLOATS, dev)
+    if q is None:
+        q = _new(shape, torch.int8, dev, other)
+    else:
+        _given("q", q, shape, torch.int8, dev)
+    if scale is None:
+        scale = _new(shape[:1], torch.float32, dev, other)
+    else:
+        _given("scale", scale, shape[:1], torch.float32, dev)
+    _lib.check("mtgr_quantize_rows", _lib.load().mtgr_quantize_rows(
+        shape[0], shape[1], _CODE[x.dtype], x.data_ptr(), ld, q.data_ptr(), scale.data_ptr(), raw))
     return q, scale
 
 
+@_on_its_device
 def linear_i8(x, w, w_scale, x_scale=None, bias=None, epi: int = MTGR_EPI_NONE, resid=None, q_cols: int = 0,
               out_dtype=torch.float32, out=None, ws=None, status=None, stream=None) -> torch.Tensor:
     """Linear layer with int8 weights ``w`` [N, K] and a scale per output channel
@@ -216,35 +261,51 @@ def linear_i8(x, w, w_scale, x_scale=None, bias=None, epi: int = MTGR_EPI_NONE, 
     [M, N] float32 and ``q_cols`` as in gemm. ``status``: a device int32 word
     (zeroed by the caller) for errors the device finds: an f16 value out of
     range, a wait that ran out; without it they go unseen."""
-    with _On(x, stream) as on:
-        _need(x.dim() == 2 and w.dim() == 2, "x: [M, K] and w: [N, K] are needed")
-        M, K = x.shape
-        N = w.shape[0]
-        on.given("w", w, (N, K), (torch.int8,))
-        on.given("w_scale", w_scale, (N,), _F32)
-        if bias is not None:
-            on.given("bias", bias, (N,), _F32)
-        if epi == MTGR_EPI_RESID:
-            _need(resid is not None, "resid is needed with MTGR_EPI_RESID")
-            on.given("resid", resid, (M, N), _F32)
-        else:
-            _need(resid is None, "resid goes with MTGR_EPI_RESID")
-        if out is None:
-            out = on.empty((M, N), out_dtype)
-        else:
-            on.given("out", out, (M, N), (out_dtype,))
-        if x.dtype == torch.int8:
-            on.given("x", x, (M, K), (torch.int8,))
-            _need(x_scale is not None, "x_scale is needed with int8 rows")
-            on.given("x_scale", x_scale, (M,), _F32)
-            _lib.mtgr_gemm_i8(x, x_scale, w, w_scale, bias, epi, resid, q_cols, out, status, on.stream)
-            return out
-        _need(x_scale is None, "x_scale goes with int8 rows")
-        on.given("x", x, (M, K), _FLOATS, rows=True)
-        need = _lib.mtgr_linear_i8_workspace_bytes(M, K)
-        if ws is None or ws.numel() < need:
-            ws = on.bytes(need)
-        _lib.mtgr_linear_i8(_rows(x), w, w_scale, bias, epi, resid, q_cols, out, ws, status, on.stream)
+    dev = x.get_device()
+    raw, other = _where(stream, dev)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x: [M, K] and w: [N, K] are needed")
+    M, K = x.shape
+    N = w.shape[0]
+    _given("w", w, (N, K), torch.int8, dev)
+    _given("w_scale", w_scale, (N,), torch.float32, dev)
+    if bias is not None:
+        _given("bias", bias, (N,), torch.float32, dev)
+    if resid is not None:
+        _given("resid", resid, (M, N), torch.float32, dev)
+    if (resid is not None) != (epi == MTGR_EPI_RESID):
+        raise ValueError("resid and MTGR_EPI_RESID come together")
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype {out_dtype}: float32, bfloat16 or float16")
+    if out is None:
+        out = _new((M, N), out_dtype, dev, other)
+    else:
+        _given("out", out, (M, N), out_dtype, dev)
+    if status is not None:
+        _given("status", status, (1,), torch.int32, dev)
+    tail = (w.data_ptr(), w_scale.data_ptr(), None if bias is None else bias.data_ptr(), epi,
+            None if resid is None else resid.data_ptr(), q_cols, _CODE[out_dtype], out.data_ptr())
+    st = None if status is None else status.data_ptr()
+    if x.dtype == torch.int8:
+        _given("x", x, (M, K), torch.int8, dev)
+        if x_scale is None:
+            raise ValueError("x_scale is needed with int8 rows")
+        _given("x_scale", x_scale, (M,), torch.float32, dev)
+        _lib.check("mtgr_gemm_i8", _lib.load().mtgr_gemm_i8(M, N, K, x.data_ptr(), x_scale.data_ptr(), *tail, st, raw))
+        return out
+    if x_scale is not None:
+        raise ValueError("x_scale goes with int8 rows")
+    ld = _given_rows("x", x, (M, K), _FLOATS, dev)
+    need = _lib.load().mtgr_linear_i8_workspace_bytes(M, K)
+    if need == 0:
+        p, room = None, 0
+    elif ws is None or ws.numel() * ws.element_size() < need:
+        ws = _new((need,), torch.uint8, dev, other)
+        p, room = ws.data_ptr(), need
+    else:
+        p, room = ws.data_ptr(), ws.numel() * ws.element_size()
+    _lib.check("mtgr_linear_i8", _lib.load().mtgr_linear_i8(M, N, K, _CODE[x.dtype], x.data_ptr(), ld, *tail, p, room, st,
+                                                            raw))
     return out
 
 
@@ -252,7 +313,8 @@ def gemm_i8(a, a_scale, b, b_scale, bias=None, epi: int = MTGR_EPI_NONE, resid=N
             out_dtype=torch.float32, out=None, status=None, stream=None) -> torch.Tensor:
     """out = epi(a_scale b_scale a b^T + bias) of int8 ``a`` [M, K] and ``b`` [N, K]
     with a scale per row of each (mtgr_gemm_i8)."""
-    _need(a.dtype == torch.int8, "a: int8 rows are needed")
+    if a.dtype != torch.int8:
+        raise ValueError("a: int8 rows are needed")
     return linear_i8(a, b, b_scale, a_scale, bias, epi, resid, q_cols, out_dtype, out, None, status, stream)
 
 
@@ -264,61 +326,59 @@ class GradientSet:
     hstu_block_backward and boundary_backward return; contiguous, of any size.
     ``outs``: where the clipped values go, tensor by tensor (the gradient's
     type or float32); None: in place. The tensors' memory is read at every
-    call, so a step writes new gradients into the same buffers.
+    call, so a step writes new gradients into the same buffers. The set's
+    workspaces and status word are its own: clips of one set are ordered by
+    the caller, two sets may run at once.
     """
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
         self.outs = self.grads if outs is None else list(outs)
-        _need(len(self.grads) == len(self.outs), "one output per gradient is needed")
-        _need(len(self.grads) > 0, "at least one gradient is needed")
+        if len(self.grads) != len(self.outs) or not self.grads:
+            raise ValueError("at least one gradient, and one output per gradient, are needed")
+        if not self.grads[0].is_cuda:
+            raise ValueError("device tensors are needed")
         self.device = self.grads[0].device
+        dev, n = self.device.index, len(self.grads)
         spans = []
-        n = len(self.grads)
         self.c = (MtgrGradTensor * n)()
-        with _On(self.grads[0], None) as on:
-            for i, (g, o) in enumerate(zip(self.grads, self.outs)):
-                on.given(f"grads[{i}]", g, g.shape, _FLOATS)
-                on.given(f"outs[{i}]", o, g.shape, (g.dtype, torch.float32))
-                self.c[i] = MtgrGradTensor(g.data_ptr(), o.data_ptr(), g.numel(), _lib.dtype_code(g.dtype),
-                                           _lib.dtype_code(o.dtype))
-                if g.numel():
-                    spans.append((o.data_ptr(), o.data_ptr() + o.numel() * o.element_size(), i, 1))
-                    if o.data_ptr() != g.data_ptr() or o.dtype != g.dtype:
-                        spans.append((g.data_ptr(), g.data_ptr() + g.numel() * g.element_size(), i, 0))
-            # no two outputs may share memory, nor an output and another gradient
-            spans.sort()
-            end_out = end_any = 0
-            for lo, hi, i, is_out in spans:
-                _need(lo >= (end_any if is_out else end_out), f"tensor {i} shares memory with another one")
-                end_any = max(end_any, hi)
-                if is_out:
-                    end_out = max(end_out, hi)
-            # the norm alone
-            self.c_norm = (MtgrGradTensor * n)(*[MtgrGradTensor(c.g, None, c.n, c.dtype, c.dtype) for c in self.c])
-            self.ws_bytes = _lib.mtgr_grad_clip_workspace_bytes(self.c, n)
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
-
-    def _run(self, table, max_norm, inv_scale, norm, status, stream):
-        with _On(self.grads[0], stream) as on:
-            if norm is None:
-                norm = on.empty((1,), torch.float32)
-            else:
-                on.given("norm", norm, (1,), _F32)
-            _lib.mtgr_grad_clip(table, len(self.grads), max_norm, inv_scale, norm, on.bytes(self.ws_bytes),
-                                self.status if status is None else status, on.stream)
-        return norm
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.dtype not in _FLOATS or o.dtype not in (g.dtype, torch.float32):
+                raise ValueError(f"tensor {i}: {g.dtype} to {o.dtype}: a float type to itself or to float32")
+            _given(f"grads[{i}]", g, g.shape, g.dtype, dev)
+            _given(f"outs[{i}]", o, g.shape, o.dtype, dev)
+            self.c[i] = MtgrGradTensor(g.data_ptr(), o.data_ptr(), g.numel(), _CODE[g.dtype], _CODE[o.dtype])
+            if g.numel():
+                spans.append((o.data_ptr(), o.data_ptr() + o.numel() * o.element_size(), i, 1))
+                if o.data_ptr() != g.data_ptr() or o.dtype != g.dtype:
+                    spans.append((g.data_ptr(), g.data_ptr() + g.numel() * g.element_size(), i, 0))
+        # no two outputs may share memory, nor an output and another gradient
+        spans.sort()
+        end_out = end_any = 0
+        for lo, hi, i, is_out in spans:
+            if lo < (end_any if is_out else end_out):
+                raise ValueError(f"tensor {i} shares memory with another one")
+            end_any = max(end_any, hi)
+            if is_out:
+                end_out = max(end_out, hi)
+        # the norm alone
+        self.c_norm = (MtgrGradTensor * n)(*[MtgrGradTensor(c.g, None, c.n, c.dtype, c.dtype) for c in self.c])
+        with torch.cuda.device(self.device):
+            # one for each of the two calls, so that a norm may run beside a clip
+            size = _lib.mtgr_grad_clip_workspace_bytes(self.c, n)
+            self.ws, self.ws_norm = (torch.empty(size, dtype=torch.uint8, device=self.device) for _ in range(2))
+            self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def clip(self, max_norm: float, inv_scale: float = 1.0, norm=None, status=None, stream=None) -> torch.Tensor:
         """Clips to ``max_norm`` after taking the loss scale out (``inv_scale`` = 1 /
         loss scale). Returns the norm before clipping ([1] float32 on the
         device). A norm that is not finite leaves the outputs as they were and
         MTGR_ERR_RANGE in ``status`` (default: the set's own word, see check)."""
-        return self._run(self.c, max_norm, inv_scale, norm, status, stream)
+        return _clip(self.ws, self, self.c, max_norm, inv_scale, norm, status, stream)
 
     def norm(self, inv_scale: float = 1.0, norm=None, status=None, stream=None) -> torch.Tensor:
         """The norm alone; nothing is written but it."""
-        return self._run(self.c_norm, float("inf"), inv_scale, norm, status, stream)
+        return _clip(self.ws_norm, self, self.c_norm, float("inf"), inv_scale, norm, status, stream)
 
     def check(self) -> None:
         """Synchronise and raise if a call on this set met a norm that is not
@@ -328,3 +388,22 @@ class GradientSet:
         if st != 0:
             self.status.zero_()
             raise _lib.MTGRError("device status", st)
+
+
+@_on_its_device
+def _clip(ws, grads, table, max_norm, inv_scale, norm, status, stream):
+    dev = ws.get_device()
+    raw, other = _where(stream, dev)
+    if norm is None:
+        norm = _new((1,), torch.float32, dev, other)
+    else:
+        _given("norm", norm, (1,), torch.float32, dev)
+    if status is None:
+        status = grads.status
+    else:
+        _given("status", status, (1,), torch.int32, dev)
+    if other is not None:
+        ws.record_stream(other)
+    _lib.check("mtgr_grad_clip", _lib.load().mtgr_grad_clip(
+        table, len(table), max_norm, inv_scale, norm.data_ptr(), ws.data_ptr(), ws.numel(), status.data_ptr(), raw))
+    return norm
