@@ -33,6 +33,18 @@ namespace {
 
 __device__ __forceinline__ float sigmoid_f32(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
 
+__device__ __forceinline__ float silu_f32(float u) { return __fdividef(u, 1.0f + __expf(-u)); }
+
+__device__ __forceinline__ bool beyond_f16(const f2 (&v)[4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpair2(v[k]);
+    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  return m > 65504.f;
+}
+
 // f(u); silu as u / (1 + e^-u): e^-u = inf gives -0, as the limit does
 __device__ __forceinline__ void gate8(int gate, const float (&u)[8], float (&f)[8]) {
   if (gate == MTGR_GATE_SILU) {
@@ -98,7 +110,7 @@ __global__ void __launch_bounds__(256) boundary_fwd_kernel(BoundaryFwdArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) q = fmaf(v[e] - mean, v[e] - mean, q);
       }
-    rstd = 1.0f / sqrtf(team.sum1(q) * inv_d + a.eps);
+    rstd = rsqrtf(team.sum1(q) * inv_d + a.eps);
   }
   float h[VPL][8];
   float s = 0.f;
@@ -150,7 +162,7 @@ __global__ void __launch_bounds__(256) boundary_fwd_kernel(BoundaryFwdArgs a) {
         q = fmaf(h[k][e], h[k][e], q);
       }
     }
-  rstd = 1.0f / sqrtf(team.sum1(q) * inv_d + a.eps);
+  rstd = rsqrtf(team.sum1(q) * inv_d + a.eps);
   uint32_t m = 0u;
 #pragma unroll
   for (int k = 0; k < VPL; ++k) {
@@ -234,25 +246,16 @@ __device__ __forceinline__ void copy8(uint32_t dst, uint32_t step, const T* src)
 #pragma unroll
   for (int i = 0; i < kPieces<T>; ++i) copy16(dst + i * step, reinterpret_cast<const char*>(src) + 16 * i);
 }
-__device__ __forceinline__ void unpack16(const uint4& a, float (&v)[8], __nv_bfloat16) {
-  Vec8<__nv_bfloat16> r;
-  r.a = a;
-  r.unpack(v);
-}
-__device__ __forceinline__ void unpack16(const uint4& a, float (&v)[8], __half) {
-  Vec8<__half> r;
-  r.a = a;
-  r.unpack(v);
-}
 template <typename T>
-__device__ __forceinline__ void read8(uint32_t src, uint32_t step, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const uint4 a = shared16(src), b = shared16(src + step);
-    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
-  } else {
-    unpack16(shared16(src), v, T());
-  }
+__device__ __forceinline__ void read8(uint32_t src, uint32_t step, f2 (&v)[4]) {
+  const uint4 a = shared16(src);
+  uint4 b = a;
+  if constexpr (sizeof(T) == 4) b = shared16(src + step);
+  to_pairs(a, b, v, T());
+}
+__device__ __forceinline__ void zero8(f2 (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = 0ull;
 }
 
 // Warps of a row's team.
@@ -261,44 +264,68 @@ inline int bwd_warps(int d) {
   return w <= 4 ? w : (w <= 8 ? 8 : (w <= 16 ? 16 : 32));
 }
 
-// Rows in flight beside the one computed: two where 16 warps' stages fit in an SM.
-template <typename TO, int WARPS>
-constexpr int kAhead = WARPS == 32 ? 0 : (WARPS == 16 || sizeof(TO) == 4 ? 1 : 2);
+// Rows in flight beside the one computed; none for the largest teams, whose rows
+// alone fill the shared memory.
+template <int WARPS>
+constexpr int kAhead = WARPS == 32 ? 0 : 1;
 
+// 16-byte pieces a thread keeps: its rows' inputs, and its columns' parameters
+// (post gamma and beta, scale, pre gamma) of the group at hand.
 template <typename TO, typename TX>
-constexpr int kRowBytes = 16 * (2 * kPieces<TO> + 2 * kPieces<TX> + 2);
+constexpr int kRowPieces = 2 * kPieces<TO> + 2 * kPieces<TX> + 2;
+// (The largest teams read the parameters from memory: no room.)
+template <int WARPS>
+constexpr int kParamPieces = WARPS == 32 ? 0 : 8;
+
+template <typename TO, typename TX, int WARPS>
+constexpr int bwd_thread_bytes() {
+  return 16 * (kParamPieces<WARPS> + (kAhead<WARPS> + 1) * kRowPieces<TO, TX>);
+}
 
 // Sums over a team: a warp, or a block of WARPS warps that meet in shared memory
 // (partials in two slots used in turn, so that one barrier a sum is enough).
 template <int WARPS>
 struct Sums {
-  float2* part;  // [2][WARPS]
+  float* part;  // [2][WARPS][2]
   int turn = 0;
-  __device__ __forceinline__ float2 operator()(float a, float b) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    return meet(make_float2(a, b));
-  }
   __device__ __forceinline__ float operator()(float a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    return meet(make_float2(a, 0.f)).x;
-  }
-  __device__ __forceinline__ float2 meet(float2 v) {
     if constexpr (WARPS > 1) {
-      float2* p = part + turn * WARPS;
-      if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = v;
+      float* p = part + turn * 2 * WARPS;
+      if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = a;
       __syncthreads();
-      v = p[0];
+      a = p[0];
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) a += p[w];
+      turn ^= 1;
+    }
+    return a;
+  }
+  // two sums for six exchanges: the lanes' halves swap one value each, and each
+  // half adds up the other value
+  __device__ __forceinline__ float2 operator()(float a, float b) {
+    const bool low = (threadIdx.x & 16) == 0;
+    const float give = low ? b : a;
+    float keep = low ? a : b;
+    keep += __shfl_xor_sync(0xffffffffu, give, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+    float2 v;
+    if constexpr (WARPS > 1) {
+      float* p = part + turn * 2 * WARPS;
+      if ((threadIdx.x & 15) == 0) p[2 * (threadIdx.x >> 5) + (low ? 0 : 1)] = keep;
+      __syncthreads();
+      v = make_float2(p[0], p[1]);
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) {
-        v.x += p[w].x;
-        v.y += p[w].y;
+        v.x += p[2 * w];
+        v.y += p[2 * w + 1];
       }
       turn ^= 1;
+    } else {
+      const float other = __shfl_xor_sync(0xffffffffu, keep, 16);
+      v = low ? make_float2(keep, other) : make_float2(other, keep);
     }
     return v;
   }
@@ -312,11 +339,11 @@ struct Sums {
 // workspace (each thread its own columns: no atomics, and the same order of sums
 // in every run).
 template <typename TO, typename TX, int WARPS>
-__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS <= 2 ? 8 / (WARPS == 1 ? 2 : 1) : (WARPS <= 16 ? 16 / WARPS : 1))
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS == 1 ? 4 : (WARPS <= 16 ? 16 / WARPS : 1))
     boundary_bwd_kernel(BoundaryBwdArgs a) {
-  constexpr int AHEAD = kAhead<TO, WARPS>;
+  constexpr int AHEAD = kAhead<WARPS>;
   extern __shared__ uint4 smem[];
-  __shared__ float2 part[2 * WARPS];
+  __shared__ float part[4 * WARPS];
   Sums<WARPS> sums{part};
   constexpr bool BLOCK = WARPS > 1;
   const int tl = BLOCK ? threadIdx.x : threadIdx.x & 31;
@@ -330,16 +357,15 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS <= 2 ? 8 
   const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr, gate = a.gate != MTGR_GATE_NONE;
   const float inv_d = 1.0f / (float)d;
   float* slots = a.part + ti * a.G * kSlots * d + c0;
-  // this thread's pieces: stage s at base + s * stage, input pieces `step` apart
-  const uint32_t step = blockDim.x * 16, stage = kRowBytes<TO, TX> / 16 * step;
-  const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+  // this thread's pieces lie `step` bytes apart: the parameters', then the stages'
+  const uint32_t step = blockDim.x * 16, stage = kRowPieces<TO, TX> * step;
+  const uint32_t params = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+  const uint32_t base = params + kParamPieces<WARPS> * step;
   constexpr int PO = kPieces<TO>, PX = kPieces<TX>;
 
-  float acc[kSlots][8];
+  f2 acc[kSlots][4];
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
+  for (int i = 0; i < kSlots; ++i) zero8(acc[i]);
   uint32_t seen = 0u;
   int g_run = -1;
   bool range_bad = false;
@@ -351,18 +377,49 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS <= 2 ? 8 
       const bool add = (seen >> g_run) & 1u;
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
-        float v[8];
         if (add) {
-          load8(p + (int64_t)i * d, v);
+          const uint4 x = *reinterpret_cast<const uint4*>(p + (int64_t)i * d);
+          const uint4 y = *reinterpret_cast<const uint4*>(p + (int64_t)i * d + 4);
+          f2 v[4];
+          to_pairs(x, y, v, 0.f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[i][e] += v[e];
+          for (int k = 0; k < 4; ++k) acc[i][k] = add2(acc[i][k], v[k]);
         }
-        store8(p + (int64_t)i * d, acc[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
+        store_pairs(p + (int64_t)i * d, acc[i]);
+        zero8(acc[i]);
       }
     }
     seen |= 1u << g_run;
+  };
+  // the group's parameters to this thread's pieces (0 past d)
+  auto take_params = [&](int g) {
+    if constexpr (WARPS == 32) return;
+    const int64_t pc = (int64_t)g * d + c0;
+    const float* src[4] = {a.post_gamma, a.post_beta, a.scale, a.pre_gamma};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+      if (on && src[i] != nullptr) {
+        x = *reinterpret_cast<const uint4*>(src[i] + pc);
+        y = *reinterpret_cast<const uint4*>(src[i] + pc + 4);
+      }
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(params + 2 * i * step), "r"(x.x), "r"(x.y),
+                   "r"(x.z), "r"(x.w) : "memory");
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(params + (2 * i + 1) * step), "r"(y.x),
+                   "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+    }
+  };
+  // the i-th parameter's values of this thread's columns
+  auto param = [&](int i, const float* src, f2 (&v)[4]) {
+    if constexpr (WARPS == 32) {
+      zero8(v);
+      if (on) {
+        const int64_t pc = (int64_t)g_run * d + c0;
+        to_pairs(*reinterpret_cast<const uint4*>(src + pc), *reinterpret_cast<const uint4*>(src + pc + 4), v, 0.f);
+      }
+    } else {
+      read8<float>(params + 2 * i * step, step, v);
+    }
   };
   auto copy_row = [&](int r, int s) {
     if (on && r < rows) {
@@ -381,6 +438,11 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS <= 2 ? 8 
     }
     copy_commit();
   };
+  // what a thread past d reads is 0 throughout, so it adds nothing to a sum
+  if (!on) {
+    for (int i = 0; i < (AHEAD + 1) * kRowPieces<TO, TX>; ++i)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + i * step), "r"(0) : "memory");
+  }
 
 #pragma unroll
   for (int r = 0; r < AHEAD; ++r) copy_row(r, r);
@@ -388,142 +450,156 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS <= 2 ? 8 
   for (int r = 0; r < rows; ++r) {
     copy_row(r + AHEAD, s == 0 ? AHEAD : s - 1);  // stage (s + AHEAD) mod (AHEAD + 1)
     const int g_next = r + 1 < rows ? clamp_group(a.gid, t0 + r + 1, a.G) : 0;
-    copy_wait<AHEAD>();
-    const uint32_t at = base + s * stage;
     if (g != g_run) {
       flush();
       g_run = g;
+      take_params(g);
     }
-    const int64_t t = t0 + r, pc = (int64_t)g * d + c0;
-    // n and f again (what is past d is 0, so that it adds nothing to a sum)
-    float oh[8] = {}, n[8], f[8], gp[8] = {}, sc[8];
+    copy_wait<AHEAD>();
+    const uint32_t at = base + s * stage;
+    const int64_t t = t0 + r;
+    // n and p = n f again
+    f2 oh[4], n[4], p[4], v[4], w[4];
     float rstd_o = 1.f;
-    if (on) read8<TO>(at, step, oh);
+    read8<TO>(at, step, oh);
     if (post) {
-      float q = 0.f, m = 0.f;
+      const float m = sums(sum_of(add2(add2(oh[0], oh[1]), add2(oh[2], oh[3])))) * inv_d;
+      f2 q = 0ull;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m += oh[e];
-      m = sums(m) * inv_d;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        oh[e] = on ? oh[e] - m : 0.f;
-        q = fmaf(oh[e], oh[e], q);
+      for (int k = 0; k < 4; ++k) {
+        oh[k] = add2(oh[k], both(-m));
+        q = fma2(oh[k], oh[k], q);
       }
-      rstd_o = 1.0f / sqrtf(sums(q) * inv_d + a.eps);
-      float bt[8] = {};
-      if (on) {
-        load8(a.post_gamma + pc, gp);
-        load8(a.post_beta + pc, bt);
-      }
+      rstd_o = rsqrtf(sums(on ? sum_of(q) : 0.f) * inv_d + a.eps);
+      param(0, a.post_gamma, v);
+      param(1, a.post_beta, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        oh[e] *= rstd_o;
-        n[e] = fmaf(oh[e], gp[e], bt[e]);
+      for (int k = 0; k < 4; ++k) {
+        oh[k] = mul2(oh[k], both(rstd_o));
+        n[k] = fma2(oh[k], v[k], w[k]);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) n[e] = oh[e];
+      for (int k = 0; k < 4; ++k) n[k] = oh[k];
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = 1.f;
+    f2 f[4];
     if (gate) {
-      float uv[8] = {};
-      if (on) read8<TO>(at + PO * step, step, uv);
-      gate8(a.gate, uv, f);
-    }
+      read8<TO>(at + PO * step, step, f);
+      if (a.gate == MTGR_GATE_SILU) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sc[e] = 1.f;
-    if (a.scale != nullptr && on) load8(a.scale + pc, sc);
+        for (int k = 0; k < 4; ++k) {
+          const float2 u = unpair2(f[k]);
+          f[k] = pair2(silu_f32(u.x), silu_f32(u.y));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = mul2(n[k], f[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[k] = both(1.f);
+        p[k] = n[k];
+      }
+    }
+    f2 sc[4];
+    if (a.scale != nullptr) {
+      param(2, a.scale, sc);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sc[k] = both(1.f);
+    }
     // H: the gradient at h
-    float H[8] = {};
+    f2 H[4];
     if (pre) {
-      float hh[8] = {}, m = 0.f, q = 0.f;
-      if (on) read8<TX>(at + 2 * PO * step, step, hh);
+      f2 hh[4], m = 0ull;
+      read8<TX>(at + 2 * PO * step, step, hh);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        hh[e] = fmaf(n[e] * f[e], sc[e], hh[e]);
-        m += hh[e];
+      for (int k = 0; k < 4; ++k) {
+        hh[k] = fma2(p[k], sc[k], hh[k]);
+        m = add2(m, hh[k]);
       }
-      m = sums(on ? m : 0.f) * inv_d;
+      const float mean = sums(sum_of(m)) * inv_d;
+      f2 q = 0ull;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        hh[e] = on ? hh[e] - m : 0.f;
-        q = fmaf(hh[e], hh[e], q);
+      for (int k = 0; k < 4; ++k) {
+        hh[k] = add2(hh[k], both(-mean));
+        q = fma2(hh[k], hh[k], q);
       }
-      const float rstd_h = 1.0f / sqrtf(sums(q) * inv_d + a.eps);
-      float dy[8] = {}, gm[8] = {};
-      if (on) {
-        if (a.dy_dtype == MTGR_F32) read8<float>(at + (2 * PO + 2 * PX) * step, step, dy);
-        else read8<__nv_bfloat16>(at + (2 * PO + 2 * PX) * step, step, dy);
-        load8(a.pre_gamma + pc, gm);
-      }
-      float m0 = 0.f, m1 = 0.f;
+      const float rstd_h = rsqrtf(sums(on ? sum_of(q) : 0.f) * inv_d + a.eps);
+      if (a.dy_dtype == MTGR_F32) read8<float>(at + (2 * PO + 2 * PX) * step, step, v);
+      else read8<__nv_bfloat16>(at + (2 * PO + 2 * PX) * step, step, v);
+      param(3, a.pre_gamma, w);
+      f2 m0 = 0ull, m1 = 0ull;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        hh[e] *= rstd_h;
-        acc[kPreGamma][e] = fmaf(dy[e], hh[e], acc[kPreGamma][e]);
-        acc[kPreBeta][e] += dy[e];
-        dy[e] *= gm[e];
-        m0 += dy[e];
-        m1 = fmaf(dy[e], hh[e], m1);
+      for (int k = 0; k < 4; ++k) {
+        hh[k] = mul2(hh[k], both(rstd_h));
+        acc[kPreGamma][k] = fma2(v[k], hh[k], acc[kPreGamma][k]);
+        acc[kPreBeta][k] = add2(acc[kPreBeta][k], v[k]);
+        v[k] = mul2(v[k], w[k]);
+        m0 = add2(m0, v[k]);
+        m1 = fma2(v[k], hh[k], m1);
       }
-      const float2 ms = sums(m0, m1);
-      m0 = ms.x * inv_d;
-      m1 = ms.y * inv_d;
+      const float2 ms = sums(sum_of(m0), sum_of(m1));
+      const f2 c0n = both(-ms.x * inv_d), c1n = both(-ms.y * inv_d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) H[e] = rstd_h * (dy[e] - m0 - hh[e] * m1);
+      for (int k = 0; k < 4; ++k) H[k] = mul2(both(rstd_h), fma2(hh[k], c1n, add2(v[k], c0n)));
+    } else {
+      zero8(H);
     }
-    if (a.dh != nullptr && on) {
-      float dh[8];
-      read8<TX>(at + (2 * PO + PX) * step, step, dh);
+    if (a.dh != nullptr) {
+      read8<TX>(at + (2 * PO + PX) * step, step, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) H[e] += dh[e];
+      for (int k = 0; k < 4; ++k) H[k] = add2(H[k], v[k]);
     }
-    if (on) store8(static_cast<TX*>(a.dx) + t * d + c0, H);
-    float b[8], m0 = 0.f, m1 = 0.f;
+    if (on) store_pairs(static_cast<TX*>(a.dx) + t * d + c0, H);
+    // sc becomes the gradient at p times the scale
+    f2 m0 = 0ull, m1 = 0ull;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc[kScale][k] = fma2(H[k], p[k], acc[kScale][k]);
+      sc[k] = mul2(H[k], sc[k]);
+    }
     if (gate) {
-      float du[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) du[e] = H[e] * sc[e] * n[e];
-      if (a.gate == MTGR_GATE_SILU && on) {
-        float uv[8];
-        read8<TO>(at + PO * step, step, uv);
+      for (int k = 0; k < 4; ++k) v[k] = mul2(sc[k], n[k]);
+      if (a.gate == MTGR_GATE_SILU) {
+        f2 u[4];
+        read8<TO>(at + PO * step, step, u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float sg = sigmoid_f32(uv[e]);
-          du[e] *= fmaf(f[e], 1.0f - sg, sg);  // sigmoid(u) (1 + u (1 - sigmoid(u)))
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = unpair2(u[k]), y = unpair2(f[k]);
+          const float s0 = sigmoid_f32(x.x), s1 = sigmoid_f32(x.y);
+          // sigmoid(u) (1 + u (1 - sigmoid(u)))
+          v[k] = mul2(v[k], pair2(fmaf(y.x, 1.0f - s0, s0), fmaf(y.y, 1.0f - s1, s1)));
         }
       }
       if (on) {
-        store8(static_cast<TO*>(a.du) + t * a.ld_du + c0, du);
-        if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) range_bad |= fabsf(du[e]) > 65504.f;
+        store_pairs(static_cast<TO*>(a.du) + t * a.ld_du + c0, v);
+        if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16) range_bad |= beyond_f16(v);
       }
     }
+    if (post) param(0, a.post_gamma, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float hf = H[e] * f[e];
-      acc[kScale][e] = fmaf(hf, n[e], acc[kScale][e]);
-      b[e] = hf * sc[e];  // dn
-      acc[kPostGamma][e] = fmaf(b[e], oh[e], acc[kPostGamma][e]);
-      acc[kPostBeta][e] += b[e];
-      b[e] = post ? b[e] * gp[e] : b[e];
-      m0 += b[e];
-      m1 = fmaf(b[e], oh[e], m1);
+    for (int k = 0; k < 4; ++k) {
+      const f2 dn = mul2(sc[k], f[k]);
+      acc[kPostGamma][k] = fma2(dn, oh[k], acc[kPostGamma][k]);
+      acc[kPostBeta][k] = add2(acc[kPostBeta][k], dn);
+      v[k] = dn;
+      if (post) {
+        v[k] = mul2(dn, w[k]);
+        m0 = add2(m0, v[k]);
+        m1 = fma2(v[k], oh[k], m1);
+      }
     }
     if (post) {
-      const float2 ms = sums(m0, m1);
-      m0 = ms.x * inv_d;
-      m1 = ms.y * inv_d;
+      const float2 ms = sums(sum_of(m0), sum_of(m1));
+      const f2 c0n = both(-ms.x * inv_d), c1n = both(-ms.y * inv_d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = rstd_o * (b[e] - m0 - oh[e] * m1);
+      for (int k = 0; k < 4; ++k) v[k] = mul2(both(rstd_o), fma2(oh[k], c1n, add2(v[k], c0n)));
     }
     if (on) {
-      store8(static_cast<TO*>(a.d_o) + t * a.ld_do + c0, b);
-      if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) range_bad |= fabsf(b[e]) > 65504.f;
+      store_pairs(static_cast<TO*>(a.d_o) + t * a.ld_do + c0, v);
+      if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16) range_bad |= beyond_f16(v);
     }
     g = g_next;
     s = s == AHEAD ? 0 : s + 1;
@@ -571,10 +647,38 @@ __global__ void __launch_bounds__(512) boundary_bwd_reduce_kernel(BoundaryBwdArg
       make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
 }
 
+// Teams of the backward: at most `resident`, at least 4 rows each, and at most
+// 256 MB of gradient slots.
+int32_t bwd_teams(int32_t T, int32_t d, int32_t G, int64_t resident) {
+  if (T <= 0) return 0;
+  int64_t teams = resident;
+  const int64_t most = (256ll << 20) / ((int64_t)G * kSlots * d * 4);
+  if (teams > most) teams = most > 0 ? most : 1;
+  const int64_t by_rows = ((int64_t)T + 3) / 4;
+  if (teams > by_rows) teams = by_rows;
+  const int64_t rows = ((int64_t)T + teams - 1) / teams;
+  return (int32_t)(((int64_t)T + rows - 1) / rows);
+}
+
+// Most teams that any form has resident at once: 16 warps an SM, by registers.
+int64_t bwd_resident(int32_t d) {
+  const int warps = bwd_warps(d);
+  return (int64_t)device_sm_count() * (warps <= 16 ? 16 / warps : 1);
+}
+
 template <typename TO, typename TX, int WARPS>
-int launch_bwd_w(const BoundaryBwdArgs& a, cudaStream_t s) {
-  const int threads = WARPS == 1 ? 128 : 32 * WARPS;
-  const int bytes = threads * (kAhead<TO, WARPS> + 1) * kRowBytes<TO, TX>;
+int launch_bwd_w(BoundaryBwdArgs& a, cudaStream_t s) {
+  constexpr int threads = WARPS == 1 ? 128 : 32 * WARPS;
+  constexpr int bytes = threads * bwd_thread_bytes<TO, TX, WARPS>();
+  // blocks an SM holds at once: by registers, and by shared memory (228 KB, 1 KB of
+  // it per block for the system); a team that waited for another to end would
+  // double the time
+  constexpr int by_regs = WARPS == 1 ? 4 : (WARPS <= 16 ? 16 / WARPS : 1);
+  constexpr int by_smem = 228 * 1024 / (bytes + 16 * WARPS + 1024);
+  static_assert(by_smem >= 1, "shared memory of a block");
+  constexpr int blocks = by_regs < by_smem ? by_regs : by_smem;
+  a.teams = bwd_teams(a.T, a.d, a.G, (int64_t)device_sm_count() * blocks * (WARPS == 1 ? 4 : 1));
+  a.rows_per_team = (a.T + a.teams - 1) / a.teams;
   auto kern = boundary_bwd_kernel<TO, TX, WARPS>;
   if (bytes > 40 * 1024 &&  // 48 KB without asking, some of it static
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
@@ -584,8 +688,8 @@ int launch_bwd_w(const BoundaryBwdArgs& a, cudaStream_t s) {
 }
 
 template <typename TO, typename TX>
-int launch_bwd_t(const BoundaryBwdArgs& a, cudaStream_t s) {
-  if (a.teams > 0) {
+int launch_bwd_t(BoundaryBwdArgs& a, cudaStream_t s) {
+  if (a.T > 0) {
     int rc = MTGR_OK;
     switch (bwd_warps(a.d)) {
       case 1: rc = launch_bwd_w<TO, TX, 1>(a, s); break;
@@ -605,23 +709,8 @@ int launch_bwd_t(const BoundaryBwdArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Teams of the backward: as many as are resident at once (16 warps an SM, by
-// registers), at least 4 rows each, and at most 256 MB of gradient slots.
-int32_t boundary_bwd_teams(int32_t T, int32_t d, int32_t G) {
-  if (T <= 0) return 0;
-  const int warps = bwd_warps(d);
-  int64_t teams = (int64_t)device_sm_count() * (16 / warps > 0 ? 16 / warps : 1);
-  const int64_t slot_bytes = (int64_t)G * kSlots * d * 4;
-  const int64_t most = (256ll << 20) / slot_bytes;
-  if (teams > most) teams = most > 0 ? most : 1;
-  const int64_t by_rows = ((int64_t)T + 3) / 4;
-  if (teams > by_rows) teams = by_rows;
-  const int64_t rows = ((int64_t)T + teams - 1) / teams;
-  return (int32_t)(((int64_t)T + rows - 1) / rows);
-}
-
 size_t boundary_bwd_ws_bytes(int32_t T, int32_t d, int32_t G) {
-  const size_t teams = (size_t)boundary_bwd_teams(T, d, G);
+  const size_t teams = (size_t)bwd_teams(T, d, G, bwd_resident(d));
   return align_up(teams * 4, 256) + teams * G * kSlots * d * 4;
 }
 
@@ -640,10 +729,10 @@ int launch_boundary_fwd(const BoundaryFwdArgs& a, int32_t o_dtype, int32_t x_dty
 }
 
 int launch_boundary_bwd(BoundaryBwdArgs a, int32_t x_dtype, void* ws, cudaStream_t s) {
-  a.teams = boundary_bwd_teams(a.T, a.d, a.G);
-  a.rows_per_team = a.teams > 0 ? (a.T + a.teams - 1) / a.teams : 0;
+  a.teams = a.rows_per_team = 0;  // set with the form
   a.seen = static_cast<uint32_t*>(ws);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up((size_t)a.teams * 4, 256));
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                    align_up((size_t)bwd_teams(a.T, a.d, a.G, bwd_resident(a.d)) * 4, 256));
   if (x_dtype == MTGR_F32) {
     if (a.o_dtype == MTGR_F32) return launch_bwd_t<float, float>(a, s);
     if (a.o_dtype == MTGR_BF16) return launch_bwd_t<__nv_bfloat16, float>(a, s);

@@ -90,6 +90,73 @@ __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// ----------------------------------------------------------- packed pairs --
+// Two fp32 values in one 64-bit register pair: sm_100 adds, multiplies and
+// multiply-adds pairs in one instruction. Eight values are four pairs.
+using f2 = uint64_t;
+__device__ __forceinline__ f2 pair2(float lo, float hi) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpair2(f2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ f2 both(float v) { return pair2(v, v); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float sum_of(f2 a) {
+  const float2 f = unpair2(a);
+  return f.x + f.y;
+}
+
+// Eight elements as loaded (one or two 16-byte words) to four pairs.
+__device__ __forceinline__ void to_pairs(const uint4& a, const uint4& b, f2 (&v)[4], float) {
+  v[0] = pair2(__uint_as_float(a.x), __uint_as_float(a.y));
+  v[1] = pair2(__uint_as_float(a.z), __uint_as_float(a.w));
+  v[2] = pair2(__uint_as_float(b.x), __uint_as_float(b.y));
+  v[3] = pair2(__uint_as_float(b.z), __uint_as_float(b.w));
+}
+__device__ __forceinline__ void to_pairs(const uint4& a, const uint4&, f2 (&v)[4], __nv_bfloat16) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = pair2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+}
+__device__ __forceinline__ void to_pairs(const uint4& a, const uint4&, f2 (&v)[4], __half) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+    v[k] = pair2(f.x, f.y);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* p, const f2 (&v)[4]) {
+  float o[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpair2(v[k]);
+    o[2 * k] = f.x;
+    o[2 * k + 1] = f.y;
+  }
+  store8(p, o);
+}
+
 // ------------------------------------------------------------------ teams --
 // A row's threads: one warp (TEAM = 32), or a whole block (TEAM = blockDim.x,
 // a multiple of 32 up to 1024), whose warps meet in shared memory. Every
