@@ -241,6 +241,11 @@ __device__ __forceinline__ uint4 shared16(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void put16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ void copy8(uint32_t dst, uint32_t step, const T* src) {
 #pragma unroll
@@ -258,28 +263,27 @@ __device__ __forceinline__ void zero8(f2 (&v)[4]) {
   for (int k = 0; k < 4; ++k) v[k] = 0ull;
 }
 
-// Warps of a row's team.
-inline int bwd_warps(int d) {
-  const int w = (d + 255) / 256;
-  return w <= 4 ? w : (w <= 8 ? 8 : (w <= 16 ? 16 : 32));
-}
-
-// Rows in flight beside the one computed; none for the largest teams, whose rows
-// alone fill the shared memory.
+// Rows in flight beside the one computed. The largest teams' rows alone fill the
+// shared memory: none ahead, and the parameters read from memory.
 template <int WARPS>
-constexpr int kAhead = WARPS == 32 ? 0 : 1;
+constexpr int kAhead = WARPS == 16 ? 0 : 1;
 
-// 16-byte pieces a thread keeps: its rows' inputs, and its columns' parameters
-// (post gamma and beta, scale, pre gamma) of the group at hand.
+// 16-byte pieces a thread keeps per vector of eight columns: its rows' inputs, and
+// the parameters (post gamma and beta, scale, pre gamma) of the group at hand.
 template <typename TO, typename TX>
 constexpr int kRowPieces = 2 * kPieces<TO> + 2 * kPieces<TX> + 2;
-// (The largest teams read the parameters from memory: no room.)
 template <int WARPS>
-constexpr int kParamPieces = WARPS == 32 ? 0 : 8;
+constexpr int kParamPieces = WARPS == 16 ? 0 : 8;
 
-template <typename TO, typename TX, int WARPS>
+template <typename TO, typename TX, int WARPS, int VPL>
 constexpr int bwd_thread_bytes() {
-  return 16 * (kParamPieces<WARPS> + (kAhead<WARPS> + 1) * kRowPieces<TO, TX>);
+  return 16 * VPL * (kParamPieces<WARPS> + (kAhead<WARPS> + 1) * kRowPieces<TO, TX>);
+}
+
+// Blocks an SM holds at once, by registers: 16 warps of one vector a thread, 8 of two.
+constexpr int bwd_blocks(int warps, int vpl) {
+  const int all = vpl == 1 ? 16 : 8, per = warps == 1 ? 4 : warps;
+  return all / per > 0 ? all / per : 1;
 }
 
 // Sums over a team: a warp, or a block of WARPS warps that meet in shared memory
@@ -332,16 +336,17 @@ struct Sums {
 };
 
 // A team takes a contiguous run of rows (a user's segments are runs of one
-// group, so the group seldom changes), one vector of eight a thread: a warp for
-// d <= 256, four to a block; above, a block of WARPS = ceil(d / 256) warps (rounded
-// up to a power of two past four). The parameter gradients gather in registers
-// while the group stays the same; then they go to the team's own slots of the
-// workspace (each thread its own columns: no atomics, and the same order of sums
-// in every run).
-template <typename TO, typename TX, int WARPS>
-__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS == 1 ? 4 : (WARPS <= 16 ? 16 / WARPS : 1))
+// group, so the group seldom changes): a warp for d <= 512, four to a block; above,
+// a block of WARPS warps. VPL vectors of eight columns a thread: two, so that a
+// thread has two independent chains and a row few exchanges (at 200003 x 512: 573
+// us with one vector and two warps a row). The parameter gradients gather in
+// registers while the group stays the same; then they go to the team's own slots
+// of the workspace (each thread its own columns: no atomics, and the same order of
+// sums in every run).
+template <typename TO, typename TX, int WARPS, int VPL>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARPS, VPL))
     boundary_bwd_kernel(BoundaryBwdArgs a) {
-  constexpr int AHEAD = kAhead<WARPS>;
+  constexpr int AHEAD = kAhead<WARPS>, PP = kParamPieces<WARPS>;
   extern __shared__ uint4 smem[];
   __shared__ float part[4 * WARPS];
   Sums<WARPS> sums{part};
@@ -350,99 +355,113 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS == 1 ? 4 
   const int64_t ti = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (ti >= a.teams) return;
   const int d = a.d;
-  const bool on = tl < (d >> 3);
+  constexpr int VSTEP = 8 * 32 * WARPS;  // columns between a thread's vectors
   const int c0 = 8 * tl;
+  bool on[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) on[j] = c0 + j * VSTEP < d;
   const int64_t t0 = ti * a.rows_per_team;
   const int rows = (int)min((int64_t)a.rows_per_team, (int64_t)a.T - t0);
   const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr, gate = a.gate != MTGR_GATE_NONE;
   const float inv_d = 1.0f / (float)d;
   float* slots = a.part + ti * a.G * kSlots * d + c0;
-  // this thread's pieces lie `step` bytes apart: the parameters', then the stages'
-  const uint32_t step = blockDim.x * 16, stage = kRowPieces<TO, TX> * step;
+  // this thread's pieces lie `step` bytes apart: the parameters', then the
+  // stages', vector by vector
+  constexpr int RP = kRowPieces<TO, TX>, PO = kPieces<TO>, PX = kPieces<TX>;
+  const uint32_t step = blockDim.x * 16, stage = VPL * RP * step;
   const uint32_t params = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
-  const uint32_t base = params + kParamPieces<WARPS> * step;
-  constexpr int PO = kPieces<TO>, PX = kPieces<TX>;
+  const uint32_t base = params + VPL * PP * step;
 
-  f2 acc[kSlots][4];
+  f2 acc[kSlots][VPL][4];
 #pragma unroll
-  for (int i = 0; i < kSlots; ++i) zero8(acc[i]);
+  for (int i = 0; i < kSlots; ++i)
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) zero8(acc[i][j]);
   uint32_t seen = 0u;
   int g_run = -1;
   bool range_bad = false;
 
   auto flush = [&]() {
     if (g_run < 0) return;
-    if (on) {
-      float* p = slots + (int64_t)g_run * kSlots * d;
-      const bool add = (seen >> g_run) & 1u;
+    float* p = slots + (int64_t)g_run * kSlots * d;
+    const bool add = (seen >> g_run) & 1u;
 #pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        if (add) {
-          const uint4 x = *reinterpret_cast<const uint4*>(p + (int64_t)i * d);
-          const uint4 y = *reinterpret_cast<const uint4*>(p + (int64_t)i * d + 4);
-          f2 v[4];
-          to_pairs(x, y, v, 0.f);
+    for (int i = 0; i < kSlots; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][k] = add2(acc[i][k], v[k]);
+      for (int j = 0; j < VPL; ++j) {
+        if (on[j]) {
+          float* q = p + (int64_t)i * d + j * VSTEP;
+          if (add) {
+            f2 v[4];
+            to_pairs(*reinterpret_cast<const uint4*>(q), *reinterpret_cast<const uint4*>(q + 4), v, 0.f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[i][j][k] = add2(acc[i][j][k], v[k]);
+          }
+          store_pairs(q, acc[i][j]);
         }
-        store_pairs(p + (int64_t)i * d, acc[i]);
-        zero8(acc[i]);
+        zero8(acc[i][j]);
       }
-    }
     seen |= 1u << g_run;
   };
   // the group's parameters to this thread's pieces (0 past d)
   auto take_params = [&](int g) {
-    if constexpr (WARPS == 32) return;
+    if constexpr (PP == 0) return;
     const int64_t pc = (int64_t)g * d + c0;
     const float* src[4] = {a.post_gamma, a.post_beta, a.scale, a.pre_gamma};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-      if (on && src[i] != nullptr) {
-        x = *reinterpret_cast<const uint4*>(src[i] + pc);
-        y = *reinterpret_cast<const uint4*>(src[i] + pc + 4);
+    for (int j = 0; j < VPL; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+        if (on[j] && src[i] != nullptr) {
+          x = *reinterpret_cast<const uint4*>(src[i] + pc + j * VSTEP);
+          y = *reinterpret_cast<const uint4*>(src[i] + pc + j * VSTEP + 4);
+        }
+        const uint32_t to = params + (j * PP + 2 * i) * step;
+        put16(to, x);
+        put16(to + step, y);
       }
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(params + 2 * i * step), "r"(x.x), "r"(x.y),
-                   "r"(x.z), "r"(x.w) : "memory");
-      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(params + (2 * i + 1) * step), "r"(y.x),
-                   "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
-    }
   };
-  // the i-th parameter's values of this thread's columns
-  auto param = [&](int i, const float* src, f2 (&v)[4]) {
-    if constexpr (WARPS == 32) {
+  auto param = [&](int i, int j, f2 (&v)[4]) {
+    if constexpr (PP == 0) {
       zero8(v);
-      if (on) {
-        const int64_t pc = (int64_t)g_run * d + c0;
-        to_pairs(*reinterpret_cast<const uint4*>(src + pc), *reinterpret_cast<const uint4*>(src + pc + 4), v, 0.f);
+      if (on[j]) {
+        const float* src = i == 0 ? a.post_gamma : i == 1 ? a.post_beta : i == 2 ? a.scale : a.pre_gamma;
+        src += (int64_t)g_run * d + c0 + j * VSTEP;
+        to_pairs(*reinterpret_cast<const uint4*>(src), *reinterpret_cast<const uint4*>(src + 4), v, 0.f);
       }
     } else {
-      read8<float>(params + 2 * i * step, step, v);
+      read8<float>(params + (j * PP + 2 * i) * step, step, v);
     }
   };
   auto copy_row = [&](int r, int s) {
-    if (on && r < rows) {
+    if (r < rows) {
       const int64_t t = t0 + r;
-      const uint32_t at = base + s * stage;
-      copy8(at, step, static_cast<const TO*>(a.o) + t * a.ld_o + c0);
-      if (gate) copy8(at + PO * step, step, static_cast<const TO*>(a.u) + t * a.ld_u + c0);
-      if (a.dh != nullptr) copy8(at + (2 * PO + PX) * step, step, static_cast<const TX*>(a.dh) + t * d + c0);
-      if (pre) {
-        copy8(at + 2 * PO * step, step, static_cast<const TX*>(a.x) + t * d + c0);
-        if (a.dy_dtype == MTGR_F32)
-          copy8(at + (2 * PO + 2 * PX) * step, step, static_cast<const float*>(a.dy) + t * d + c0);
-        else
-          copy8(at + (2 * PO + 2 * PX) * step, step, static_cast<const __nv_bfloat16*>(a.dy) + t * d + c0);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        if (!on[j]) continue;
+        const int c = c0 + j * VSTEP;
+        const uint32_t at = base + s * stage + j * RP * step;
+        copy8(at, step, static_cast<const TO*>(a.o) + t * a.ld_o + c);
+        if (gate) copy8(at + PO * step, step, static_cast<const TO*>(a.u) + t * a.ld_u + c);
+        if (a.dh != nullptr) copy8(at + (2 * PO + PX) * step, step, static_cast<const TX*>(a.dh) + t * d + c);
+        if (pre) {
+          copy8(at + 2 * PO * step, step, static_cast<const TX*>(a.x) + t * d + c);
+          if (a.dy_dtype == MTGR_F32)
+            copy8(at + (2 * PO + 2 * PX) * step, step, static_cast<const float*>(a.dy) + t * d + c);
+          else
+            copy8(at + (2 * PO + 2 * PX) * step, step, static_cast<const __nv_bfloat16*>(a.dy) + t * d + c);
+        }
       }
     }
     copy_commit();
   };
-  // what a thread past d reads is 0 throughout, so it adds nothing to a sum
-  if (!on) {
-    for (int i = 0; i < (AHEAD + 1) * kRowPieces<TO, TX>; ++i)
-      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + i * step), "r"(0) : "memory");
-  }
+  // what is read past d is 0 throughout, so it adds nothing to a sum
+#pragma unroll
+  for (int j = 0; j < VPL; ++j)
+    if (!on[j])
+      for (int s = 0; s <= AHEAD; ++s)
+        for (int i = 0; i < RP; ++i) put16(base + s * stage + (j * RP + i) * step, make_uint4(0u, 0u, 0u, 0u));
 
 #pragma unroll
   for (int r = 0; r < AHEAD; ++r) copy_row(r, r);
@@ -459,147 +478,189 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, WARPS == 1 ? 4 
     const uint32_t at = base + s * stage;
     const int64_t t = t0 + r;
     // n and p = n f again
-    f2 oh[4], n[4], p[4], v[4], w[4];
+    f2 oh[VPL][4], n[VPL][4], p[VPL][4], v[VPL][4], w[4];
     float rstd_o = 1.f;
-    read8<TO>(at, step, oh);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) read8<TO>(at + j * RP * step, step, oh[j]);
     if (post) {
-      const float m = sums(sum_of(add2(add2(oh[0], oh[1]), add2(oh[2], oh[3])))) * inv_d;
       f2 q = 0ull;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        oh[k] = add2(oh[k], both(-m));
-        q = fma2(oh[k], oh[k], q);
-      }
-      rstd_o = rsqrtf(sums(on ? sum_of(q) : 0.f) * inv_d + a.eps);
-      param(0, a.post_gamma, v);
-      param(1, a.post_beta, w);
+      for (int j = 0; j < VPL; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        oh[k] = mul2(oh[k], both(rstd_o));
-        n[k] = fma2(oh[k], v[k], w[k]);
-      }
-    } else {
+        for (int k = 0; k < 4; ++k) q = add2(q, oh[j][k]);
+      const f2 m = both(-sums(sum_of(q)) * inv_d);
+      float sq = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) n[k] = oh[k];
-    }
-    f2 f[4];
-    if (gate) {
-      read8<TO>(at + PO * step, step, f);
-      if (a.gate == MTGR_GATE_SILU) {
+      for (int j = 0; j < VPL; ++j) {
+        q = 0ull;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 u = unpair2(f[k]);
-          f[k] = pair2(silu_f32(u.x), silu_f32(u.y));
+          oh[j][k] = add2(oh[j][k], m);
+          q = fma2(oh[j][k], oh[j][k], q);
+        }
+        sq += on[j] ? sum_of(q) : 0.f;
+      }
+      rstd_o = rsqrtf(sums(sq) * inv_d + a.eps);
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        param(0, j, v[j]);
+        param(1, j, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          oh[j][k] = mul2(oh[j][k], both(rstd_o));
+          n[j][k] = fma2(oh[j][k], v[j][k], w[k]);
         }
       }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) p[k] = mul2(n[k], f[k]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[k] = both(1.f);
-        p[k] = n[k];
-      }
+      for (int j = 0; j < VPL; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) n[j][k] = oh[j][k];
     }
-    f2 sc[4];
-    if (a.scale != nullptr) {
-      param(2, a.scale, sc);
-    } else {
+    f2 f[VPL][4], sc[VPL][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sc[k] = both(1.f);
+    for (int j = 0; j < VPL; ++j) {
+      if (gate) {
+        read8<TO>(at + (j * RP + PO) * step, step, f[j]);
+        if (a.gate == MTGR_GATE_SILU) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 u = unpair2(f[j][k]);
+            f[j][k] = pair2(silu_f32(u.x), silu_f32(u.y));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[j][k] = mul2(n[j][k], f[j][k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[j][k] = both(1.f);
+          p[j][k] = n[j][k];
+        }
+      }
+      if (a.scale != nullptr) {
+        param(2, j, sc[j]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sc[j][k] = both(1.f);
+      }
     }
     // H: the gradient at h
-    f2 H[4];
+    f2 H[VPL][4];
     if (pre) {
-      f2 hh[4], m = 0ull;
-      read8<TX>(at + 2 * PO * step, step, hh);
+      f2 hh[VPL][4], m = 0ull;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        hh[k] = fma2(p[k], sc[k], hh[k]);
-        m = add2(m, hh[k]);
-      }
-      const float mean = sums(sum_of(m)) * inv_d;
-      f2 q = 0ull;
+      for (int j = 0; j < VPL; ++j) {
+        read8<TX>(at + (j * RP + 2 * PO) * step, step, hh[j]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        hh[k] = add2(hh[k], both(-mean));
-        q = fma2(hh[k], hh[k], q);
+        for (int k = 0; k < 4; ++k) {
+          hh[j][k] = fma2(p[j][k], sc[j][k], hh[j][k]);
+          m = add2(m, hh[j][k]);
+        }
       }
-      const float rstd_h = rsqrtf(sums(on ? sum_of(q) : 0.f) * inv_d + a.eps);
-      if (a.dy_dtype == MTGR_F32) read8<float>(at + (2 * PO + 2 * PX) * step, step, v);
-      else read8<__nv_bfloat16>(at + (2 * PO + 2 * PX) * step, step, v);
-      param(3, a.pre_gamma, w);
+      const f2 mean = both(-sums(sum_of(m)) * inv_d);
+      float sq = 0.f;
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        f2 q = 0ull;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          hh[j][k] = add2(hh[j][k], mean);
+          q = fma2(hh[j][k], hh[j][k], q);
+        }
+        sq += on[j] ? sum_of(q) : 0.f;
+      }
+      const float rstd_h = rsqrtf(sums(sq) * inv_d + a.eps);
       f2 m0 = 0ull, m1 = 0ull;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        hh[k] = mul2(hh[k], both(rstd_h));
-        acc[kPreGamma][k] = fma2(v[k], hh[k], acc[kPreGamma][k]);
-        acc[kPreBeta][k] = add2(acc[kPreBeta][k], v[k]);
-        v[k] = mul2(v[k], w[k]);
-        m0 = add2(m0, v[k]);
-        m1 = fma2(v[k], hh[k], m1);
+      for (int j = 0; j < VPL; ++j) {
+        const uint32_t from = at + (j * RP + 2 * PO + 2 * PX) * step;
+        if (a.dy_dtype == MTGR_F32) read8<float>(from, step, v[j]);
+        else read8<__nv_bfloat16>(from, step, v[j]);
+        param(3, j, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          hh[j][k] = mul2(hh[j][k], both(rstd_h));
+          acc[kPreGamma][j][k] = fma2(v[j][k], hh[j][k], acc[kPreGamma][j][k]);
+          acc[kPreBeta][j][k] = add2(acc[kPreBeta][j][k], v[j][k]);
+          v[j][k] = mul2(v[j][k], w[k]);
+          m0 = add2(m0, v[j][k]);
+          m1 = fma2(v[j][k], hh[j][k], m1);
+        }
       }
       const float2 ms = sums(sum_of(m0), sum_of(m1));
       const f2 c0n = both(-ms.x * inv_d), c1n = both(-ms.y * inv_d);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) H[k] = mul2(both(rstd_h), fma2(hh[k], c1n, add2(v[k], c0n)));
-    } else {
-      zero8(H);
-    }
-    if (a.dh != nullptr) {
-      read8<TX>(at + (2 * PO + PX) * step, step, v);
+      for (int j = 0; j < VPL; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) H[k] = add2(H[k], v[k]);
+        for (int k = 0; k < 4; ++k) H[j][k] = mul2(both(rstd_h), fma2(hh[j][k], c1n, add2(v[j][k], c0n)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) zero8(H[j]);
     }
-    if (on) store_pairs(static_cast<TX*>(a.dx) + t * d + c0, H);
-    // sc becomes the gradient at p times the scale
     f2 m0 = 0ull, m1 = 0ull;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      acc[kScale][k] = fma2(H[k], p[k], acc[kScale][k]);
-      sc[k] = mul2(H[k], sc[k]);
-    }
-    if (gate) {
+    for (int j = 0; j < VPL; ++j) {
+      const int c = c0 + j * VSTEP;
+      if (a.dh != nullptr) {
+        read8<TX>(at + (j * RP + 2 * PO + PX) * step, step, v[j]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = mul2(sc[k], n[k]);
-      if (a.gate == MTGR_GATE_SILU) {
-        f2 u[4];
-        read8<TO>(at + PO * step, step, u);
+        for (int k = 0; k < 4; ++k) H[j][k] = add2(H[j][k], v[j][k]);
+      }
+      if (on[j]) store_pairs(static_cast<TX*>(a.dx) + t * d + c, H[j]);
+      // sc becomes the gradient at p
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 x = unpair2(u[k]), y = unpair2(f[k]);
-          const float s0 = sigmoid_f32(x.x), s1 = sigmoid_f32(x.y);
-          // sigmoid(u) (1 + u (1 - sigmoid(u)))
-          v[k] = mul2(v[k], pair2(fmaf(y.x, 1.0f - s0, s0), fmaf(y.y, 1.0f - s1, s1)));
+      for (int k = 0; k < 4; ++k) {
+        acc[kScale][j][k] = fma2(H[j][k], p[j][k], acc[kScale][j][k]);
+        sc[j][k] = mul2(H[j][k], sc[j][k]);
+      }
+      if (gate) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[j][k] = mul2(sc[j][k], n[j][k]);
+        if (a.gate == MTGR_GATE_SILU) {
+          f2 u[4];
+          read8<TO>(at + (j * RP + PO) * step, step, u);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = unpair2(u[k]), y = unpair2(f[j][k]);
+            const float s0 = sigmoid_f32(x.x), s1 = sigmoid_f32(x.y);
+            // sigmoid(u) (1 + u (1 - sigmoid(u)))
+            v[j][k] = mul2(v[j][k], pair2(fmaf(y.x, 1.0f - s0, s0), fmaf(y.y, 1.0f - s1, s1)));
+          }
+        }
+        if (on[j]) {
+          store_pairs(static_cast<TO*>(a.du) + t * a.ld_du + c, v[j]);
+          if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16) range_bad |= beyond_f16(v[j]);
         }
       }
-      if (on) {
-        store_pairs(static_cast<TO*>(a.du) + t * a.ld_du + c0, v);
-        if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16) range_bad |= beyond_f16(v);
-      }
-    }
-    if (post) param(0, a.post_gamma, w);
+      if (post) param(0, j, w);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const f2 dn = mul2(sc[k], f[k]);
-      acc[kPostGamma][k] = fma2(dn, oh[k], acc[kPostGamma][k]);
-      acc[kPostBeta][k] = add2(acc[kPostBeta][k], dn);
-      v[k] = dn;
-      if (post) {
-        v[k] = mul2(dn, w[k]);
-        m0 = add2(m0, v[k]);
-        m1 = fma2(v[k], oh[k], m1);
+      for (int k = 0; k < 4; ++k) {
+        const f2 dn = mul2(sc[j][k], f[j][k]);
+        acc[kPostGamma][j][k] = fma2(dn, oh[j][k], acc[kPostGamma][j][k]);
+        acc[kPostBeta][j][k] = add2(acc[kPostBeta][j][k], dn);
+        v[j][k] = dn;
+        if (post) {
+          v[j][k] = mul2(dn, w[k]);
+          m0 = add2(m0, v[j][k]);
+          m1 = fma2(v[j][k], oh[j][k], m1);
+        }
       }
     }
     if (post) {
       const float2 ms = sums(sum_of(m0), sum_of(m1));
       const f2 c0n = both(-ms.x * inv_d), c1n = both(-ms.y * inv_d);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = mul2(both(rstd_o), fma2(oh[k], c1n, add2(v[k], c0n)));
+      for (int j = 0; j < VPL; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[j][k] = mul2(both(rstd_o), fma2(oh[j][k], c1n, add2(v[j][k], c0n)));
     }
-    if (on) {
-      store_pairs(static_cast<TO*>(a.d_o) + t * a.ld_do + c0, v);
-      if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16) range_bad |= beyond_f16(v);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      if (on[j]) {
+        store_pairs(static_cast<TO*>(a.d_o) + t * a.ld_do + c0 + j * VSTEP, v[j]);
+        if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16) range_bad |= beyond_f16(v[j]);
+      }
     }
     g = g_next;
     s = s == AHEAD ? 0 : s + 1;
@@ -660,26 +721,30 @@ int32_t bwd_teams(int32_t T, int32_t d, int32_t G, int64_t resident) {
   return (int32_t)(((int64_t)T + rows - 1) / rows);
 }
 
-// Most teams that any form has resident at once: 16 warps an SM, by registers.
+// Warps of a row's team and vectors a thread.
+inline int bwd_warps(int d) { return d <= 512 ? 1 : (d <= 1024 ? 2 : (d <= 2048 ? 4 : (d <= 4096 ? 8 : 16))); }
+inline int bwd_vpl(int d) { return d <= 256 ? 1 : 2; }
+
+// Most teams that any types of this width have resident at once.
 int64_t bwd_resident(int32_t d) {
   const int warps = bwd_warps(d);
-  return (int64_t)device_sm_count() * (warps <= 16 ? 16 / warps : 1);
+  return (int64_t)device_sm_count() * bwd_blocks(warps, bwd_vpl(d)) * (warps == 1 ? 4 : 1);
 }
 
-template <typename TO, typename TX, int WARPS>
+template <typename TO, typename TX, int WARPS, int VPL>
 int launch_bwd_w(BoundaryBwdArgs& a, cudaStream_t s) {
   constexpr int threads = WARPS == 1 ? 128 : 32 * WARPS;
-  constexpr int bytes = threads * bwd_thread_bytes<TO, TX, WARPS>();
+  constexpr int bytes = threads * bwd_thread_bytes<TO, TX, WARPS, VPL>();
   // blocks an SM holds at once: by registers, and by shared memory (228 KB, 1 KB of
   // it per block for the system); a team that waited for another to end would
   // double the time
-  constexpr int by_regs = WARPS == 1 ? 4 : (WARPS <= 16 ? 16 / WARPS : 1);
   constexpr int by_smem = 228 * 1024 / (bytes + 16 * WARPS + 1024);
   static_assert(by_smem >= 1, "shared memory of a block");
+  constexpr int by_regs = bwd_blocks(WARPS, VPL);
   constexpr int blocks = by_regs < by_smem ? by_regs : by_smem;
   a.teams = bwd_teams(a.T, a.d, a.G, (int64_t)device_sm_count() * blocks * (WARPS == 1 ? 4 : 1));
   a.rows_per_team = (a.T + a.teams - 1) / a.teams;
-  auto kern = boundary_bwd_kernel<TO, TX, WARPS>;
+  auto kern = boundary_bwd_kernel<TO, TX, WARPS, VPL>;
   if (bytes > 40 * 1024 &&  // 48 KB without asking, some of it static
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return MTGR_ERR_CUDA;
@@ -691,15 +756,12 @@ template <typename TO, typename TX>
 int launch_bwd_t(BoundaryBwdArgs& a, cudaStream_t s) {
   if (a.T > 0) {
     int rc = MTGR_OK;
-    switch (bwd_warps(a.d)) {
-      case 1: rc = launch_bwd_w<TO, TX, 1>(a, s); break;
-      case 2: rc = launch_bwd_w<TO, TX, 2>(a, s); break;
-      case 3: rc = launch_bwd_w<TO, TX, 3>(a, s); break;
-      case 4: rc = launch_bwd_w<TO, TX, 4>(a, s); break;
-      case 8: rc = launch_bwd_w<TO, TX, 8>(a, s); break;
-      case 16: rc = launch_bwd_w<TO, TX, 16>(a, s); break;
-      default: rc = launch_bwd_w<TO, TX, 32>(a, s); break;
-    }
+    if (a.d <= 256) rc = launch_bwd_w<TO, TX, 1, 1>(a, s);
+    else if (a.d <= 512) rc = launch_bwd_w<TO, TX, 1, 2>(a, s);
+    else if (a.d <= 1024) rc = launch_bwd_w<TO, TX, 2, 2>(a, s);
+    else if (a.d <= 2048) rc = launch_bwd_w<TO, TX, 4, 2>(a, s);
+    else if (a.d <= 4096) rc = launch_bwd_w<TO, TX, 8, 2>(a, s);
+    else rc = launch_bwd_w<TO, TX, 16, 2>(a, s);
     if (rc != MTGR_OK) return rc;
   }
   const int64_t n = (int64_t)a.G * kSlots * a.d;
