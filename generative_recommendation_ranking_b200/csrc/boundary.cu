@@ -235,27 +235,18 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 shared16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-
-__device__ __forceinline__ void put16(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
 template <typename T>
-__device__ __forceinline__ void copy8(uint32_t dst, uint32_t step, const T* src) {
+__device__ __forceinline__ void copy8(uint4* dst, int step, const T* src) {
 #pragma unroll
-  for (int i = 0; i < kPieces<T>; ++i) copy16(dst + i * step, reinterpret_cast<const char*>(src) + 16 * i);
+  for (int i = 0; i < kPieces<T>; ++i)
+    copy16((uint32_t)__cvta_generic_to_shared(dst + i * step), reinterpret_cast<const char*>(src) + 16 * i);
 }
+// plain loads: the compiler may move them ahead of the exchanges before them
 template <typename T>
-__device__ __forceinline__ void read8(uint32_t src, uint32_t step, f2 (&v)[4]) {
-  const uint4 a = shared16(src);
+__device__ __forceinline__ void read8(const uint4* src, int step, f2 (&v)[4]) {
+  const uint4 a = src[0];
   uint4 b = a;
-  if constexpr (sizeof(T) == 4) b = shared16(src + step);
+  if constexpr (sizeof(T) == 4) b = src[step];
   to_pairs(a, b, v, T());
 }
 __device__ __forceinline__ void zero8(f2 (&v)[4]) {
@@ -365,12 +356,12 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
   const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr, gate = a.gate != MTGR_GATE_NONE;
   const float inv_d = 1.0f / (float)d;
   float* slots = a.part + ti * a.G * kSlots * d + c0;
-  // this thread's pieces lie `step` bytes apart: the parameters', then the
+  // this thread's pieces lie `step` pieces apart (its neighbours' between them): the parameters', then the
   // stages', vector by vector
   constexpr int RP = kRowPieces<TO, TX>, PO = kPieces<TO>, PX = kPieces<TX>;
-  const uint32_t step = blockDim.x * 16, stage = VPL * RP * step;
-  const uint32_t params = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
-  const uint32_t base = params + VPL * PP * step;
+  constexpr int step = WARPS == 1 ? 128 : 32 * WARPS, stage = VPL * RP * step;
+  uint4* params = smem + threadIdx.x;
+  uint4* base = params + VPL * PP * step;
 
   f2 acc[kSlots][VPL][4];
 #pragma unroll
@@ -417,9 +408,9 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
           x = *reinterpret_cast<const uint4*>(src[i] + pc + j * VSTEP);
           y = *reinterpret_cast<const uint4*>(src[i] + pc + j * VSTEP + 4);
         }
-        const uint32_t to = params + (j * PP + 2 * i) * step;
-        put16(to, x);
-        put16(to + step, y);
+        uint4* to = params + (j * PP + 2 * i) * step;
+        to[0] = x;
+        to[step] = y;
       }
   };
   auto param = [&](int i, int j, f2 (&v)[4]) {
@@ -441,7 +432,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
       for (int j = 0; j < VPL; ++j) {
         if (!on[j]) continue;
         const int c = c0 + j * VSTEP;
-        const uint32_t at = base + s * stage + j * RP * step;
+        uint4* at = base + s * stage + j * RP * step;
         copy8(at, step, static_cast<const TO*>(a.o) + t * a.ld_o + c);
         if (gate) copy8(at + PO * step, step, static_cast<const TO*>(a.u) + t * a.ld_u + c);
         if (a.dh != nullptr) copy8(at + (2 * PO + PX) * step, step, static_cast<const TX*>(a.dh) + t * d + c);
@@ -461,7 +452,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
   for (int j = 0; j < VPL; ++j)
     if (!on[j])
       for (int s = 0; s <= AHEAD; ++s)
-        for (int i = 0; i < RP; ++i) put16(base + s * stage + (j * RP + i) * step, make_uint4(0u, 0u, 0u, 0u));
+        for (int i = 0; i < RP; ++i) base[s * stage + (j * RP + i) * step] = make_uint4(0u, 0u, 0u, 0u);
 
 #pragma unroll
   for (int r = 0; r < AHEAD; ++r) copy_row(r, r);
@@ -475,7 +466,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
       take_params(g);
     }
     copy_wait<AHEAD>();
-    const uint32_t at = base + s * stage;
+    const uint4* at = base + s * stage;
     const int64_t t = t0 + r;
     // n and p = n f again
     f2 oh[VPL][4], n[VPL][4], p[VPL][4], v[VPL][4], w[4];
@@ -574,7 +565,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
       f2 m0 = 0ull, m1 = 0ull;
 #pragma unroll
       for (int j = 0; j < VPL; ++j) {
-        const uint32_t from = at + (j * RP + 2 * PO + 2 * PX) * step;
+        const uint4* from = at + (j * RP + 2 * PO + 2 * PX) * step;
         if (a.dy_dtype == MTGR_F32) read8<float>(from, step, v[j]);
         else read8<__nv_bfloat16>(from, step, v[j]);
         param(3, j, w);
