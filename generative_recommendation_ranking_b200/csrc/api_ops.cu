@@ -168,12 +168,15 @@ MTGR_API int mtgr_gemm_i8(int32_t M, int32_t N, int32_t K, const int8_t* d_a, co
   if ((M > 0 && N > 0 && (d_a == nullptr || d_a_scale == nullptr)) || !aligned16(d_a)) return MTGR_ERR_INVALID_ARG;
   if (!device_is_sm100()) return MTGR_ERR_UNSUPPORTED;
   TimedScope tsc(MTGR_TIMER_GEMM_QKVU, as_stream(stream), M > 0 && N > 0 ? 1 : 0);
+  if (gemm_i8_is_few(M, K))
+    return launch_gemm_i8_few(M, N, K, MTGR_I8, d_a, K, d_a_scale, d_b, d_b_scale, d_bias, epi, d_resid, q_cols,
+                              out_dtype, d_out, d_status, as_stream(stream));
   return launch_gemm_i8(M, N, K, d_a, d_a_scale, d_b, d_b_scale, d_bias, epi, d_resid, q_cols, out_dtype, d_out,
                         d_status, as_stream(stream));
 }
 
 MTGR_API size_t mtgr_linear_i8_workspace_bytes(int32_t M, int32_t K) {
-  if (M < 0 || K <= 0) return 0;
+  if (M < 0 || K <= 0 || gemm_i8_is_few(M, K)) return 0;
   return align_up((size_t)M * (size_t)K, 256) + align_up((size_t)M * 4, 256);
 }
 
@@ -185,10 +188,16 @@ MTGR_API int mtgr_linear_i8(int32_t M, int32_t N, int32_t K, int32_t x_dtype, co
   if (rc != MTGR_OK) return rc;
   rc = quant_check(M, K, x_dtype, d_x, ld_x);
   if (rc != MTGR_OK) return rc;
-  if (ws_bytes < mtgr_linear_i8_workspace_bytes(M, K)) return MTGR_ERR_CAPACITY;
-  if ((M > 0 && d_ws == nullptr) || !aligned16(d_ws)) return MTGR_ERR_INVALID_ARG;
+  const size_t need = mtgr_linear_i8_workspace_bytes(M, K);
+  if (ws_bytes < need) return MTGR_ERR_CAPACITY;
+  if ((need > 0 && d_ws == nullptr) || !aligned16(d_ws)) return MTGR_ERR_INVALID_ARG;
   if (!device_is_sm100()) return MTGR_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return MTGR_OK;
+  if (need == 0) {
+    TimedScope tsc(MTGR_TIMER_GEMM_QKVU, as_stream(stream), 1);
+    return launch_gemm_i8_few(M, N, K, x_dtype, d_x, ld_x, nullptr, d_w, d_w_scale, d_bias, epi, d_resid, q_cols,
+                              out_dtype, d_out, d_status, as_stream(stream));
+  }
   int8_t* q = static_cast<int8_t*>(d_ws);
   float* sa = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + align_up((size_t)M * (size_t)K, 256));
   {
@@ -198,7 +207,7 @@ MTGR_API int mtgr_linear_i8(int32_t M, int32_t N, int32_t K, int32_t x_dtype, co
   }
   TimedScope tsc(MTGR_TIMER_GEMM_QKVU, as_stream(stream), 1);
   return launch_gemm_i8(M, N, K, q, sa, d_w, d_w_scale, d_bias, epi, d_resid, q_cols, out_dtype, d_out, d_status,
-                        as_stream(stream));
+                        as_stream(stream), true);
 }
 
 MTGR_API size_t mtgr_grad_clip_workspace_bytes(const mtgr_grad_tensor* h_grads, int32_t n) {

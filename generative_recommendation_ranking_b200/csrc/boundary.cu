@@ -338,6 +338,7 @@ template <typename TO, typename TX, int WARPS, int VPL>
 __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARPS, VPL))
     boundary_bwd_kernel(BoundaryBwdArgs a) {
   constexpr int AHEAD = kAhead<WARPS>, PP = kParamPieces<WARPS>;
+  dependents_may_launch();
   extern __shared__ uint4 smem[];
   __shared__ float part[4 * WARPS];
   Sums<WARPS> sums{part};
@@ -662,19 +663,25 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
 }
 
 // The parameter gradients: each of the G * 5 * d columns summed over the teams
-// that saw its group, a block per 128 columns, 16 warps over the teams in a
-// fixed order, in fp64.
+// that saw its group, in fp64 and a fixed order: a block per 32 columns, four a
+// thread, its 64 groups of eight threads over the teams.
 __global__ void __launch_bounds__(512) boundary_bwd_reduce_kernel(BoundaryBwdArgs a) {
-  __shared__ double red[16][32][4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ double red[64][8][4];
+  const int cl = threadIdx.x & 7, part = threadIdx.x >> 3;
   const int64_t n = (int64_t)a.G * kSlots * a.d;
-  const int64_t c = ((int64_t)blockIdx.x * 32 + lane) * 4;  // d % 8 == 0: one slot and group per 4 columns
+  const int64_t c = ((int64_t)blockIdx.x * 8 + cl) * 4;  // d % 8 == 0: one slot and group per 4 columns
   const int gs = c < n ? (int)(c / a.d) : 0;
   const int g = gs / kSlots, slot = gs % kSlots;
+  float* out = slot == kPreGamma    ? a.g_pre_gamma
+               : slot == kPreBeta   ? a.g_pre_beta
+               : slot == kScale     ? a.g_scale
+               : slot == kPostGamma ? a.g_post_gamma
+                                    : a.g_post_beta;
+  dependent_wait();
   double s[4] = {0.0, 0.0, 0.0, 0.0};
-  if (c < n) {
+  if (c < n && out != nullptr) {
 #pragma unroll 4
-    for (int i = warp; i < a.teams; i += 16) {
+    for (int i = part; i < a.teams; i += 64) {
       if ((a.seen[i] >> g) & 1u) {
         const float4 v = *reinterpret_cast<const float4*>(a.part + i * n + c);
         s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
@@ -682,21 +689,24 @@ __global__ void __launch_bounds__(512) boundary_bwd_reduce_kernel(BoundaryBwdArg
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) red[warp][lane][k] = s[k];
+  for (int k = 0; k < 4; ++k) red[part][cl][k] = s[k];
   __syncthreads();
-  if (warp != 0 || c >= n) return;
+  // 32 columns, 16 threads each over four partials, then across the 16
+  const int col = threadIdx.x >> 4, w = threadIdx.x & 15;
+  double t = 0.0;
 #pragma unroll
-  for (int w = 1; w < 16; ++w)
+  for (int k = 0; k < 4; ++k) t += red[4 * w + k][col >> 2][col & 3];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s[k] += red[w][lane][k];
-  float* out = slot == kPreGamma    ? a.g_pre_gamma
-               : slot == kPreBeta   ? a.g_pre_beta
-               : slot == kScale     ? a.g_scale
-               : slot == kPostGamma ? a.g_post_gamma
+  for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  const int64_t cc = (int64_t)blockIdx.x * 32 + col;
+  if (w != 0 || cc >= n) return;
+  const int gs2 = (int)(cc / a.d), slot2 = gs2 % kSlots;
+  float* to = slot2 == kPreGamma    ? a.g_pre_gamma
+              : slot2 == kPreBeta   ? a.g_pre_beta
+              : slot2 == kScale     ? a.g_scale
+              : slot2 == kPostGamma ? a.g_post_gamma
                                     : a.g_post_beta;
-  if (out == nullptr) return;
-  *reinterpret_cast<float4*>(out + (int64_t)g * a.d + (c - (int64_t)gs * a.d)) =
-      make_float4((float)s[0], (float)s[1], (float)s[2], (float)s[3]);
+  if (to != nullptr) to[(int64_t)(gs2 / kSlots) * a.d + (cc - (int64_t)gs2 * a.d)] = (float)t;
 }
 
 // Teams of the backward: at most `resident`, at least 4 rows each, and at most
@@ -756,8 +766,7 @@ int launch_bwd_t(BoundaryBwdArgs& a, cudaStream_t s) {
     if (rc != MTGR_OK) return rc;
   }
   const int64_t n = (int64_t)a.G * kSlots * a.d;
-  boundary_bwd_reduce_kernel<<<(unsigned)((n + 127) / 128), 512, 0, s>>>(a);
-  return launch_status();
+  return launch_dependent(boundary_bwd_reduce_kernel, (unsigned)((n + 31) / 32), 512, 0, s, a);
 }
 
 }  // namespace

@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   bool timed_out = false;
+  dependent_wait();  // a's bytes and scales may be another kernel's of the same call
 
   if (warp == 0) {
     if (lane == 0) {
@@ -431,7 +432,7 @@ constexpr int kMaxDevices = 64;
 
 template <int EPI, int OUT, int CG>
 int launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const Args& args,
-             cudaStream_t s) {
+             cudaStream_t s, bool dependent) {
   using E = Epi<OUT, CG>;
   auto kern = gemm_i8_kernel<EPI, OUT, CG>;
   // per device: blocks (pairs) resident at once; 0 until the first launch there
@@ -442,13 +443,15 @@ int launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to
   cfg.blockDim = dim3(E::kThreads);
   cfg.dynamicSmemBytes = E::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CG;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
+  cfg.numAttrs = 1;
   int units = resident[dev].load(std::memory_order_relaxed);
   if (units == 0) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)E::kSmem) != cudaSuccess)
@@ -466,13 +469,14 @@ int launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to
                         ((args.N + Shape<CG>::kBN - 1) / Shape<CG>::kBN);
   if (tiles > 0x3fffffff) return MTGR_ERR_UNSUPPORTED;  // the kernel counts tiles in 32 bits
   cfg.gridDim = dim3((unsigned)(CG * (tiles < units ? tiles : units)));
+  cfg.numAttrs = dependent ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, ta, tb, to, args) != cudaSuccess) return MTGR_ERR_CUDA;
   return launch_status();
 }
 
 template <int CG>
 int launch_cg(int M, int N, int K, const int8_t* a, const int8_t* b, int epi, int32_t out_dtype, void* out,
-              const Args& args, cudaStream_t s) {
+              const Args& args, cudaStream_t s, bool dependent) {
   using S = Shape<CG>;
   CUtensorMap ta, tb, to;
   int rc = make_tmap_2d(&ta, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)M, (uint64_t)K, BK, BM,
@@ -488,7 +492,7 @@ int launch_cg(int M, int N, int K, const int8_t* a, const int8_t* b, int epi, in
                           (uint64_t)N * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc != MTGR_OK) return rc;
 #define MTGR_FORM(E, O) \
-  if (epi == E && out_dtype == O) return launch_t<E, O, CG>(ta, tb, to, args, s)
+  if (epi == E && out_dtype == O) return launch_t<E, O, CG>(ta, tb, to, args, s, dependent)
   MTGR_FORM(MTGR_EPI_NONE, MTGR_F16);
   MTGR_FORM(MTGR_EPI_NONE, MTGR_BF16);
   MTGR_FORM(MTGR_EPI_NONE, MTGR_F32);
@@ -505,13 +509,13 @@ int launch_cg(int M, int N, int K, const int8_t* a, const int8_t* b, int epi, in
 // K % 16 == 0, N % 8 == 0, 16-byte aligned operands.
 int launch_gemm_i8(int M, int N, int K, const int8_t* a, const float* sa, const int8_t* b, const float* sb,
                    const float* bias, int epi, const float* resid, int q_cols, int32_t out_dtype, void* out,
-                   int32_t* status, cudaStream_t s) {
+                   int32_t* status, cudaStream_t s, bool dependent) {
   if (M == 0 || N == 0) return MTGR_OK;
   const Args args{M, N, K, sa, sb, bias, resid, q_cols, status};
   // pair tiles once they fill every SM; below, the small tiles spread the work
   const int64_t pair_tiles = (((int64_t)M + 255) / 256) * ((N + 255) / 256);
-  if (2 * pair_tiles >= device_sm_count()) return launch_cg<2>(M, N, K, a, b, epi, out_dtype, out, args, s);
-  return launch_cg<1>(M, N, K, a, b, epi, out_dtype, out, args, s);
+  if (2 * pair_tiles >= device_sm_count()) return launch_cg<2>(M, N, K, a, b, epi, out_dtype, out, args, s, dependent);
+  return launch_cg<1>(M, N, K, a, b, epi, out_dtype, out, args, s, dependent);
 }
 
 }  // namespace mtgr

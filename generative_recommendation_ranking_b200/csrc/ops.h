@@ -10,6 +10,30 @@
 
 namespace mtgr {
 
+// A kernel that follows another of the same call may be launched while that one
+// still runs: its blocks take their places and wait (dependent_wait, before their
+// first access to memory) until the first kernel has ended and its writes are
+// seen. The first one allows it as soon as all of its blocks run.
+__device__ __forceinline__ void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline int launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                            A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, P(args)...) != cudaSuccess) return MTGR_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? MTGR_OK : MTGR_ERR_CUDA;
+}
+
 constexpr int kMaxGroups = 32;  // the backward keeps the groups a team saw in 32 bits
 
 struct BoundaryFwdArgs {
@@ -50,7 +74,13 @@ int launch_quantize_rows(int32_t M, int32_t K, int32_t x_dtype, const void* x, i
 // out[m][n] = epi(sa[m] sb[n] sum_k a[m][k] b[n][k] + bias[n])
 int launch_gemm_i8(int M, int N, int K, const int8_t* a, const float* sa, const int8_t* b,
                    const float* sb, const float* bias, int epi, const float* resid, int q_cols,
-                   int32_t out_dtype, void* out, int32_t* status, cudaStream_t s);
+                   int32_t out_dtype, void* out, int32_t* status, cudaStream_t s, bool dependent = false);
+
+// the same in one kernel from float rows or bytes (MTGR_I8, with sa), for few rows
+bool gemm_i8_is_few(int32_t M, int32_t K);
+int launch_gemm_i8_few(int M, int N, int K, int32_t x_dtype, const void* x, int64_t ld_x, const float* sa,
+                       const int8_t* b, const float* sb, const float* bias, int epi, const float* resid, int q_cols,
+                       int32_t out_dtype, void* out, int32_t* status, cudaStream_t s);
 
 size_t grad_clip_ws_bytes(const mtgr_grad_tensor* g, int32_t n);
 int grad_clip_launches(const mtgr_grad_tensor* g, int32_t n);

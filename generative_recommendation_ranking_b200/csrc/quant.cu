@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
   constexpr bool BLOCK = THREADS != 32;
   __shared__ float part[BLOCK ? 2 : 1][1][32];
   Team<1, BLOCK> team(part);
+  dependents_may_launch();
   const int tl = threadIdx.x % THREADS;
   const int64_t m = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (m >= M) return;

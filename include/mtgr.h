@@ -762,8 +762,9 @@ MTGR_API int mtgr_gemm_i8(int32_t M, int32_t N, int32_t K, const int8_t* d_a, co
 
 /*
  * Linear layer with int8 weights: quantises the rows of x as mtgr_quantize_rows
- * into the workspace (mtgr_linear_i8_workspace_bytes) and multiplies as
- * mtgr_gemm_i8; the arguments and limits are theirs.
+ * into the workspace (mtgr_linear_i8_workspace_bytes; 0 for few rows, which are
+ * quantised within the product's kernel, and d_ws may then be NULL) and multiplies
+ * as mtgr_gemm_i8; the arguments and limits are theirs.
  */
 MTGR_API size_t mtgr_linear_i8_workspace_bytes(int32_t M, int32_t K);
 MTGR_API int mtgr_linear_i8(int32_t M, int32_t N, int32_t K, int32_t x_dtype, const void* d_x,

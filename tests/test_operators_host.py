@@ -114,7 +114,7 @@ def test_int8_product_refusals(lib):
     def gemm(M=8, N=64, K=64, a=F, sa=F, b=F, sb=F, bias=F, epi=0, resid=None, q_cols=0, od=BF16, out=F):
         return lib.mtgr_gemm_i8(M, N, K, a, sa, b, sb, bias, epi, resid, q_cols, od, out, None, None)
 
-    def linear(M=8, N=64, K=64, xd=BF16, x=F, ld=64, b=F, sb=F, bias=F, epi=0, resid=None, q_cols=0, od=BF16, out=F, ws=F,
+    def linear(M=100, N=64, K=64, xd=BF16, x=F, ld=64, b=F, sb=F, bias=F, epi=0, resid=None, q_cols=0, od=BF16, out=F, ws=F,
                ws_bytes=1 << 20):
         return lib.mtgr_linear_i8(M, N, K, xd, x, ld, b, sb, bias, epi, resid, q_cols, od, out, ws, ws_bytes, None, None)
 
@@ -131,6 +131,7 @@ def test_int8_product_refusals(lib):
     assert linear(x=None) == INVALID and linear(ld=8) == INVALID and linear(xd=I8) == UNSUPPORTED
     assert linear(ws=None) == INVALID and linear(ws_bytes=100) == CAPACITY
     assert _lib.mtgr_linear_i8_workspace_bytes(100, 48) == 4864 + 512
+    assert _lib.mtgr_linear_i8_workspace_bytes(64, 512) == 0 and _lib.mtgr_linear_i8_workspace_bytes(64, 4096) > 0
     assert _lib.mtgr_linear_i8_workspace_bytes(-1, 48) == 0 and _lib.mtgr_linear_i8_workspace_bytes(5, 0) == 0
     assert _lib.mtgr_linear_i8_workspace_bytes(1 << 20, 8192) == (1 << 33) + (1 << 22)
 
