@@ -33,6 +33,7 @@ namespace {
 
 __device__ __forceinline__ float sigmoid_f32(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
 
+// silu as u / (1 + e^-u): e^-u = inf gives -0, as the limit does
 __device__ __forceinline__ float silu_f32(float u) { return __fdividef(u, 1.0f + __expf(-u)); }
 
 __device__ __forceinline__ bool beyond_f16(const f2 (&v)[4]) {
@@ -45,236 +46,29 @@ __device__ __forceinline__ bool beyond_f16(const f2 (&v)[4]) {
   return m > 65504.f;
 }
 
-// f(u); silu as u / (1 + e^-u): e^-u = inf gives -0, as the limit does
-__device__ __forceinline__ void gate8(int gate, const float (&u)[8], float (&f)[8]) {
-  if (gate == MTGR_GATE_SILU) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = __fdividef(u[e], 1.0f + __expf(-u[e]));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = u[e];
-  }
-}
-
 __device__ __forceinline__ int clamp_group(const int8_t* gid, int64_t t, int G) {
   const int g = gid[t];
   return g < 0 ? 0 : (g >= G ? G - 1 : g);
 }
 
-// ---------------------------------------------------------------- forward --
-// One row per warp (d <= 1024) or per block of 256 (d <= 8192), VPL vectors of
-// eight per thread; a row is read once and stays in registers through both norms.
-template <typename TO, typename TX, bool BLOCK, int VPL>
-__global__ void __launch_bounds__(256) boundary_fwd_kernel(BoundaryFwdArgs a) {
-  __shared__ float part[BLOCK ? 2 : 1][1][32];
-  Team<1, BLOCK> team(part);
-  constexpr int TS = BLOCK ? 256 : 32;
-  const int tl = threadIdx.x % TS;
-  const int64_t t = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const int d = a.d, nv = d >> 3;
-  const TO* o = static_cast<const TO*>(a.o) + t * a.ld_o;
-  const TO* u = static_cast<const TO*>(a.u) + t * a.ld_u;
-  const TX* x = static_cast<const TX*>(a.x) + t * d;
-  Vec8<TO> ro[VPL], ru[VPL];
-  Vec8<TX> rx[VPL];
-#pragma unroll
-  for (int k = 0; k < VPL; ++k) {
-    const int vi = tl + TS * k;
-    if (vi < nv) {
-      ro[k].load(o + 8 * vi);
-      rx[k].load(x + 8 * vi);
-      if (a.gate != MTGR_GATE_NONE) ru[k].load(u + 8 * vi);
-    }
-  }
-  const int g = clamp_group(a.gid, t, a.G);
-  const float inv_d = 1.0f / (float)d;
-  float mean = 0.f, rstd = 1.f;
-  if (a.post_gamma != nullptr) {
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < VPL; ++k)
-      if (tl + TS * k < nv) {
-        float v[8];
-        ro[k].unpack(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[e];
-      }
-    mean = team.sum1(s) * inv_d;
-    float q = 0.f;
-#pragma unroll
-    for (int k = 0; k < VPL; ++k)
-      if (tl + TS * k < nv) {
-        float v[8];
-        ro[k].unpack(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(v[e] - mean, v[e] - mean, q);
-      }
-    rstd = rsqrtf(team.sum1(q) * inv_d + a.eps);
-  }
-  float h[VPL][8];
-  float s = 0.f;
-#pragma unroll
-  for (int k = 0; k < VPL; ++k) {
-    const int vi = tl + TS * k;
-    if (vi >= nv) continue;
-    const int64_t pc = (int64_t)g * d + 8 * vi;
-    float n[8];
-    ro[k].unpack(n);
-    if (a.post_gamma != nullptr) {
-      float gm[8], bt[8];
-      load8(a.post_gamma + pc, gm);
-      load8(a.post_beta + pc, bt);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) n[e] = fmaf((n[e] - mean) * rstd, gm[e], bt[e]);
-    }
-    if (a.gate != MTGR_GATE_NONE) {
-      float uv[8], f[8];
-      ru[k].unpack(uv);
-      gate8(a.gate, uv, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) n[e] *= f[e];
-    }
-    float xv[8];
-    rx[k].unpack(xv);
-    if (a.scale != nullptr) {
-      float sc[8];
-      load8(a.scale + pc, sc);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = fmaf(n[e], sc[e], xv[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[k][e] = n[e] + xv[e];
-    }
-    store8(static_cast<TX*>(a.h) + t * d + 8 * vi, h[k]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s += h[k][e];
-  }
-  if (a.pre_gamma == nullptr) return;
-  mean = team.sum1(s) * inv_d;
-  float q = 0.f;
-#pragma unroll
-  for (int k = 0; k < VPL; ++k)
-    if (tl + TS * k < nv) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[k][e] -= mean;
-        q = fmaf(h[k][e], h[k][e], q);
-      }
-    }
-  rstd = rsqrtf(team.sum1(q) * inv_d + a.eps);
-  uint32_t m = 0u;
-#pragma unroll
-  for (int k = 0; k < VPL; ++k) {
-    const int vi = tl + TS * k;
-    if (vi >= nv) continue;
-    const int64_t pc = (int64_t)g * d + 8 * vi;
-    float gm[8], bt[8];
-    load8(a.pre_gamma + pc, gm);
-    load8(a.pre_beta + pc, bt);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[k][e] = fmaf(h[k][e] * rstd, gm[e], bt[e]);
-    if (a.y_dtype == MTGR_F32) {
-      store8(static_cast<float*>(a.y) + t * d + 8 * vi, h[k]);
-    } else if (a.y_dtype == MTGR_BF16) {
-      store8(static_cast<__nv_bfloat16*>(a.y) + t * d + 8 * vi, h[k]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(fabsf(h[k][e])));
-    }
-  }
-  if (a.y_dtype != MTGR_I8) return;
-  const RowScale rs = row_scale(team.max_bits(m));
-  if (tl == 0) a.y_scale[t] = rs.s;
-#pragma unroll
-  for (int k = 0; k < VPL; ++k) {
-    const int vi = tl + TS * k;
-    if (vi < nv) *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.y) + t * d + 8 * vi) = quant8(h[k], rs);
-  }
-}
-
-template <typename TO, typename TX>
-int launch_fwd_t(const BoundaryFwdArgs& a, cudaStream_t s) {
-  if (a.d <= 1024) {
-    const unsigned grid = (unsigned)(((int64_t)a.T + 7) / 8);
-    switch ((a.d + 255) / 256) {
-      case 1: boundary_fwd_kernel<TO, TX, false, 1><<<grid, 256, 0, s>>>(a); break;
-      case 2: boundary_fwd_kernel<TO, TX, false, 2><<<grid, 256, 0, s>>>(a); break;
-      case 3: boundary_fwd_kernel<TO, TX, false, 3><<<grid, 256, 0, s>>>(a); break;
-      default: boundary_fwd_kernel<TO, TX, false, 4><<<grid, 256, 0, s>>>(a); break;
-    }
-  } else {
-    switch ((a.d + 2047) / 2048) {
-      case 1: boundary_fwd_kernel<TO, TX, true, 1><<<a.T, 256, 0, s>>>(a); break;
-      case 2: boundary_fwd_kernel<TO, TX, true, 2><<<a.T, 256, 0, s>>>(a); break;
-      case 3: boundary_fwd_kernel<TO, TX, true, 3><<<a.T, 256, 0, s>>>(a); break;
-      default: boundary_fwd_kernel<TO, TX, true, 4><<<a.T, 256, 0, s>>>(a); break;
-    }
-  }
-  return launch_status();
-}
-
-// --------------------------------------------------------------- backward --
-// Gradient slots of the workspace, per team and group.
-constexpr int kSlots = 5;
-enum { kPreGamma = 0, kPreBeta = 1, kScale = 2, kPostGamma = 3, kPostBeta = 4 };
-
-// A row's inputs wait in shared memory: each thread copies its own eight values of
-// every input up to two rows ahead (cp.async) and reads back only those, so no barrier
-// is needed, and the registers hold the sums instead. Stage layout: per thread
-// o, u (16 or 32 bytes), x, dh, dy; a thread's 16-byte pieces lie THREADS * 16
-// bytes apart, so that a warp's accesses fall in different banks.
+// 16-byte pieces of eight values: 1 or 2
 template <typename T>
-constexpr int kPieces = sizeof(T) / 2;  // 16-byte pieces of eight values: 1 or 2
+constexpr int kPieces = sizeof(T) / 2;
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 template <typename T>
-__device__ __forceinline__ void copy8(uint4* dst, int step, const T* src) {
+__device__ __forceinline__ void fetch8(bool on, const T* p, uint4 (&r)[kPieces<T>]) {
 #pragma unroll
   for (int i = 0; i < kPieces<T>; ++i)
-    copy16((uint32_t)__cvta_generic_to_shared(dst + i * step), reinterpret_cast<const char*>(src) + 16 * i);
-}
-// plain loads: the compiler may move them ahead of the exchanges before them
-template <typename T>
-__device__ __forceinline__ void read8(const uint4* src, int step, f2 (&v)[4]) {
-  const uint4 a = src[0];
-  uint4 b = a;
-  if constexpr (sizeof(T) == 4) b = src[step];
-  to_pairs(a, b, v, T());
+    r[i] = on ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
 }
 __device__ __forceinline__ void zero8(f2 (&v)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] = 0ull;
 }
-
-// Rows in flight beside the one computed. The largest teams' rows alone fill the
-// shared memory: none ahead, and the parameters read from memory.
-template <int WARPS>
-constexpr int kAhead = WARPS == 16 ? 0 : 1;
-
-// 16-byte pieces a thread keeps per vector of eight columns: its rows' inputs, and
-// the parameters (post gamma and beta, scale, pre gamma) of the group at hand.
-template <typename TO, typename TX>
-constexpr int kRowPieces = 2 * kPieces<TO> + 2 * kPieces<TX> + 2;
-template <int WARPS>
-constexpr int kParamPieces = WARPS == 16 ? 0 : 8;
-
-template <typename TO, typename TX, int WARPS, int VPL>
-constexpr int bwd_thread_bytes() {
-  return 16 * VPL * (kParamPieces<WARPS> + (kAhead<WARPS> + 1) * kRowPieces<TO, TX>);
-}
-
-// Blocks an SM holds at once, by registers: 16 warps of one vector a thread, 8 of two.
-constexpr int bwd_blocks(int warps, int vpl) {
-  const int all = vpl == 1 ? 16 : 8, per = warps == 1 ? 4 : warps;
-  return all / per > 0 ? all / per : 1;
+__device__ __forceinline__ void load_param(bool on, const float* p, f2 (&v)[4]) {
+  uint4 r[2];
+  fetch8<float>(on, p, r);
+  to_pairs(r[0], r[1], v, 0.f);
 }
 
 // Sums over a team: a warp, or a block of WARPS warps that meet in shared memory
@@ -324,7 +118,220 @@ struct Sums {
     }
     return v;
   }
+  // maximum of non-negative values by their bits: a NaN is above every number
+  // and an infinity, so it is not lost
+  __device__ __forceinline__ uint32_t max_bits(uint32_t a) {
+    a = __reduce_max_sync(0xffffffffu, a);
+    if constexpr (WARPS > 1) {
+      float* p = part + turn * 2 * WARPS;
+      if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = __uint_as_float(a);
+      __syncthreads();
+      a = __float_as_uint(p[0]);
+#pragma unroll
+      for (int w = 1; w < WARPS; ++w) a = max(a, __float_as_uint(p[w]));
+      turn ^= 1;
+    }
+    return a;
+  }
 };
+
+// ---------------------------------------------------------------- forward --
+// A row per warp (d <= 512, eight rows a block) or per block of WARPS warps, VPL
+// vectors of eight columns a thread; a row is read once and stays in registers
+// through both norms. Two vectors a thread: at 65537 x 1024 with int8 y, one warp a
+// row with four took 226 us (16 warps an SM, by registers).
+template <typename TO, typename TX, int WARPS, int VPL>
+__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) boundary_fwd_kernel(BoundaryFwdArgs a) {
+  constexpr bool BLOCK = WARPS > 1;
+  __shared__ float part[BLOCK ? 4 * WARPS : 1];
+  Sums<WARPS> sums{part};
+  const int tl = BLOCK ? threadIdx.x : threadIdx.x & 31;
+  const int64_t t = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const int d = a.d;
+  constexpr int VSTEP = 8 * 32 * WARPS;  // columns between a thread's vectors
+  const int c0 = 8 * tl;
+  const bool gate = a.gate != MTGR_GATE_NONE;
+  uint4 ro[VPL][kPieces<TO>], ru[VPL][kPieces<TO>], rx[VPL][kPieces<TX>];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int c = c0 + j * VSTEP;
+    const bool on = c < d;
+    fetch8<TO>(on, static_cast<const TO*>(a.o) + t * a.ld_o + c, ro[j]);
+    fetch8<TX>(on, static_cast<const TX*>(a.x) + t * d + c, rx[j]);
+    fetch8<TO>(on && gate, static_cast<const TO*>(a.u) + t * a.ld_u + c, ru[j]);
+  }
+  const int g = clamp_group(a.gid, t, a.G);
+  const int64_t pc = (int64_t)g * d + c0;
+  const float inv_d = 1.0f / (float)d;
+  f2 h[VPL][4], v[4], w[4];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) to_pairs(ro[j][0], ro[j][kPieces<TO> - 1], h[j], TO());
+  // the rows' mean and 1 / sigma; h becomes the centred row (0 past d)
+  auto centre = [&]() {
+    f2 q = 0ull;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q = add2(q, h[j][k]);
+    const f2 m = both(-sums(sum_of(q)) * inv_d);
+    float sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      q = 0ull;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h[j][k] = add2(h[j][k], m);
+        q = fma2(h[j][k], h[j][k], q);
+      }
+      sq += c0 + j * VSTEP < d ? sum_of(q) : 0.f;
+    }
+    return rsqrtf(sums(sq) * inv_d + a.eps);
+  };
+  const bool post = a.post_gamma != nullptr;
+  const float rstd_o = post ? centre() : 1.f;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int c = c0 + j * VSTEP;
+    const bool on = c < d;
+    if (post) {
+      load_param(on, a.post_gamma + pc + j * VSTEP, v);
+      load_param(on, a.post_beta + pc + j * VSTEP, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[j][k] = fma2(mul2(h[j][k], both(rstd_o)), v[k], w[k]);
+    }
+    if (gate) {
+      to_pairs(ru[j][0], ru[j][kPieces<TO> - 1], v, TO());
+      if (a.gate == MTGR_GATE_SILU) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 u = unpair2(v[k]);
+          v[k] = pair2(silu_f32(u.x), silu_f32(u.y));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[j][k] = mul2(h[j][k], v[k]);
+    }
+    to_pairs(rx[j][0], rx[j][kPieces<TX> - 1], v, TX());
+    if (a.scale != nullptr) {
+      load_param(on, a.scale + pc + j * VSTEP, w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[j][k] = fma2(h[j][k], w[k], v[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[j][k] = add2(h[j][k], v[k]);
+    }
+    if (on) store_pairs(static_cast<TX*>(a.h) + t * d + c, h[j]);
+    else zero8(h[j]);
+  }
+  if (a.pre_gamma == nullptr) return;
+  const float rstd_h = centre();
+  uint32_t m = 0u;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int c = c0 + j * VSTEP;
+    const bool on = c < d;
+    load_param(on, a.pre_gamma + pc + j * VSTEP, v);
+    load_param(on, a.pre_beta + pc + j * VSTEP, w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[j][k] = fma2(mul2(h[j][k], both(rstd_h)), v[k], w[k]);
+    if (a.y_dtype == MTGR_F32) {
+      if (on) store_pairs(static_cast<float*>(a.y) + t * d + c, h[j]);
+    } else if (a.y_dtype == MTGR_BF16) {
+      if (on) store_pairs(static_cast<__nv_bfloat16*>(a.y) + t * d + c, h[j]);
+    } else if (on) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpair2(h[j][k]);
+        m = max(m, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
+      }
+    }
+  }
+  if (a.y_dtype != MTGR_I8) return;
+  const RowScale rs = row_scale(sums.max_bits(m));
+  if (tl == 0) a.y_scale[t] = rs.s;
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    const int c = c0 + j * VSTEP;
+    if (c < d) {
+      float y[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpair2(h[j][k]);
+        y[2 * k] = f.x;
+        y[2 * k + 1] = f.y;
+      }
+      *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.y) + t * d + c) = quant8(y, rs);
+    }
+  }
+}
+
+template <typename TO, typename TX>
+int launch_fwd_t(const BoundaryFwdArgs& a, cudaStream_t s) {
+  const unsigned rows8 = (unsigned)(((int64_t)a.T + 7) / 8);
+  if (a.d <= 256) boundary_fwd_kernel<TO, TX, 1, 1><<<rows8, 256, 0, s>>>(a);
+  else if (a.d <= 512) boundary_fwd_kernel<TO, TX, 1, 2><<<rows8, 256, 0, s>>>(a);
+  else if (a.d <= 1024) boundary_fwd_kernel<TO, TX, 2, 2><<<a.T, 64, 0, s>>>(a);
+  else if (a.d <= 2048) boundary_fwd_kernel<TO, TX, 4, 2><<<a.T, 128, 0, s>>>(a);
+  else if (a.d <= 4096) boundary_fwd_kernel<TO, TX, 8, 2><<<a.T, 256, 0, s>>>(a);
+  else boundary_fwd_kernel<TO, TX, 16, 2><<<a.T, 512, 0, s>>>(a);
+  return launch_status();
+}
+
+// --------------------------------------------------------------- backward --
+// Gradient slots of the workspace, per team and group.
+constexpr int kSlots = 5;
+enum { kPreGamma = 0, kPreBeta = 1, kScale = 2, kPostGamma = 3, kPostBeta = 4 };
+
+// A row's inputs wait in shared memory: each thread copies its own eight values of
+// every input up to two rows ahead (cp.async) and reads back only those, so no barrier
+// is needed, and the registers hold the sums instead. Stage layout: per thread
+// o, u (16 or 32 bytes), x, dh, dy; a thread's 16-byte pieces lie THREADS * 16
+// bytes apart, so that a warp's accesses fall in different banks.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void copy8(uint4* dst, int step, const T* src) {
+#pragma unroll
+  for (int i = 0; i < kPieces<T>; ++i)
+    copy16((uint32_t)__cvta_generic_to_shared(dst + i * step), reinterpret_cast<const char*>(src) + 16 * i);
+}
+// plain loads: the compiler may move them ahead of the exchanges before them
+template <typename T>
+__device__ __forceinline__ void read8(const uint4* src, int step, f2 (&v)[4]) {
+  const uint4 a = src[0];
+  uint4 b = a;
+  if constexpr (sizeof(T) == 4) b = src[step];
+  to_pairs(a, b, v, T());
+}
+// Rows in flight beside the one computed. The largest teams' rows alone fill the
+// shared memory: none ahead, and the parameters read from memory.
+template <int WARPS>
+constexpr int kAhead = WARPS == 16 ? 0 : 1;
+
+// 16-byte pieces a thread keeps per vector of eight columns: its rows' inputs, and
+// the parameters (post gamma and beta, scale, pre gamma) of the group at hand.
+template <typename TO, typename TX>
+constexpr int kRowPieces = 2 * kPieces<TO> + 2 * kPieces<TX> + 2;
+template <int WARPS>
+constexpr int kParamPieces = WARPS == 16 ? 0 : 8;
+
+template <typename TO, typename TX, int WARPS, int VPL>
+constexpr int bwd_thread_bytes() {
+  return 16 * VPL * (kParamPieces<WARPS> + (kAhead<WARPS> + 1) * kRowPieces<TO, TX>);
+}
+
+// Blocks an SM holds at once, by registers: 16 warps of one vector a thread, 8 of two.
+constexpr int bwd_blocks(int warps, int vpl) {
+  const int all = vpl == 1 ? 16 : 8, per = warps == 1 ? 4 : warps;
+  return all / per > 0 ? all / per : 1;
+}
 
 // A team takes a contiguous run of rows (a user's segments are runs of one
 // group, so the group seldom changes): a warp for d <= 512, four to a block; above,
