@@ -328,6 +328,9 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
     constexpr int NB = E::kBlocks;
     const int grp = ew >> 2;
     uint8_t* stg = sStg + ew * E::kBufs * E::kStg;
+    // the output is not read here: its lines leave L2 first (154 -> 152.7 us at
+    // 131075 x 2048 x 512 to f16)
+    const uint64_t evict_first = policy_evict_first();
     int acc = 0;
     uint32_t acc_phase = 0, chunk = 0;
     // the residual comes by plain loads into a ring of two blocks, ahead of use
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&tmO, st, col0, row0);
+            tma_store_2d_hint(&tmO, st, col0, row0, evict_first);
             bulk_commit_group();
           }
           ++chunk;
