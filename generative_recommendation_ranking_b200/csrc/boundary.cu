@@ -71,15 +71,17 @@ __device__ __forceinline__ void load_param(bool on, const float* p, f2 (&v)[4]) 
   to_pairs(r[0], r[1], v, 0.f);
 }
 
-// Sums over a team: a warp, or a block of WARPS warps that meet in shared memory
-// (partials in two slots used in turn, so that one barrier a sum is enough).
-template <int WARPS>
+// Sums over a team: LANES lanes of a warp, or a block of WARPS warps that meet in
+// shared memory (partials in two slots used in turn, so that one barrier a sum is
+// enough).
+template <int WARPS, int LANES>
 struct Sums {
+  static_assert(WARPS == 1 || LANES == 32, "a block's team is whole warps");
   float* part;  // [2][WARPS][2]
   int turn = 0;
   __device__ __forceinline__ float operator()(float a) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     if constexpr (WARPS > 1) {
       float* p = part + turn * 2 * WARPS;
       if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = a;
@@ -91,15 +93,16 @@ struct Sums {
     }
     return a;
   }
-  // two sums for six exchanges: the lanes' halves swap one value each, and each
-  // half adds up the other value
+  // two sums for half the exchanges: the lanes' halves swap one value each, and
+  // each half adds up the other value
   __device__ __forceinline__ float2 operator()(float a, float b) {
-    const bool low = (threadIdx.x & 16) == 0;
+    constexpr int HALF = LANES / 2;
+    const bool low = (threadIdx.x & HALF) == 0;
     const float give = low ? b : a;
     float keep = low ? a : b;
-    keep += __shfl_xor_sync(0xffffffffu, give, 16);
+    keep += __shfl_xor_sync(0xffffffffu, give, HALF);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
+    for (int o = HALF / 2; o > 0; o >>= 1) keep += __shfl_xor_sync(0xffffffffu, keep, o);
     float2 v;
     if constexpr (WARPS > 1) {
       float* p = part + turn * 2 * WARPS;
@@ -113,7 +116,7 @@ struct Sums {
       }
       turn ^= 1;
     } else {
-      const float other = __shfl_xor_sync(0xffffffffu, keep, 16);
+      const float other = __shfl_xor_sync(0xffffffffu, keep, HALF);
       v = low ? make_float2(keep, other) : make_float2(other, keep);
     }
     return v;
@@ -121,7 +124,12 @@ struct Sums {
   // maximum of non-negative values by their bits: a NaN is above every number
   // and an infinity, so it is not lost
   __device__ __forceinline__ uint32_t max_bits(uint32_t a) {
-    a = __reduce_max_sync(0xffffffffu, a);
+    if constexpr (LANES < 32) {
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    } else {
+      a = __reduce_max_sync(0xffffffffu, a);
+    }
     if constexpr (WARPS > 1) {
       float* p = part + turn * 2 * WARPS;
       if ((threadIdx.x & 31) == 0) p[threadIdx.x >> 5] = __uint_as_float(a);
@@ -136,20 +144,20 @@ struct Sums {
 };
 
 // ---------------------------------------------------------------- forward --
-// A row per warp (d <= 512, eight rows a block) or per block of WARPS warps, VPL
-// vectors of eight columns a thread; a row is read once and stays in registers
+// A row per team: LANES lanes of a warp (8 for d <= 64, 16 for d <= 128, 32 up to 512),
+// or a block of WARPS warps, VPL vectors of eight columns a thread; a row is read once and stays in registers
 // through both norms. Two vectors a thread: at 65537 x 1024 with int8 y, one warp a
 // row with four took 226 us (16 warps an SM, by registers).
-template <typename TO, typename TX, int WARPS, int VPL>
+template <typename TO, typename TX, int WARPS, int LANES, int VPL>
 __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) boundary_fwd_kernel(BoundaryFwdArgs a) {
   constexpr bool BLOCK = WARPS > 1;
   __shared__ float part[BLOCK ? 4 * WARPS : 1];
-  Sums<WARPS> sums{part};
-  const int tl = BLOCK ? threadIdx.x : threadIdx.x & 31;
-  const int64_t t = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const int d = a.d;
-  constexpr int VSTEP = 8 * 32 * WARPS;  // columns between a thread's vectors
+  Sums<WARPS, LANES> sums{part};
+  const int tl = BLOCK ? threadIdx.x : threadIdx.x % LANES;
+  const int64_t t = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  if (LANES == 32 && t >= a.T) return;
+  const int d = t < a.T ? a.d : 0;  // a team without a row has no columns, but goes along
+  constexpr int VSTEP = 8 * LANES * WARPS;  // columns between a thread's vectors
   const int c0 = 8 * tl;
   const bool gate = a.gate != MTGR_GATE_NONE;
   uint4 ro[VPL][kPieces<TO>], ru[VPL][kPieces<TO>], rx[VPL][kPieces<TX>];
@@ -161,9 +169,9 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) boundary_fwd_ke
     fetch8<TX>(on, static_cast<const TX*>(a.x) + t * d + c, rx[j]);
     fetch8<TO>(on && gate, static_cast<const TO*>(a.u) + t * a.ld_u + c, ru[j]);
   }
-  const int g = clamp_group(a.gid, t, a.G);
+  const int g = d > 0 ? clamp_group(a.gid, t, a.G) : 0;
   const int64_t pc = (int64_t)g * d + c0;
-  const float inv_d = 1.0f / (float)d;
+  const float inv_d = 1.0f / (float)a.d;
   f2 h[VPL][4], v[4], w[4];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) to_pairs(ro[j][0], ro[j][kPieces<TO> - 1], h[j], TO());
@@ -249,7 +257,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) boundary_fwd_ke
   }
   if (a.y_dtype != MTGR_I8) return;
   const RowScale rs = row_scale(sums.max_bits(m));
-  if (tl == 0) a.y_scale[t] = rs.s;
+  if (tl == 0 && d > 0) a.y_scale[t] = rs.s;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     const int c = c0 + j * VSTEP;
@@ -268,13 +276,15 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) boundary_fwd_ke
 
 template <typename TO, typename TX>
 int launch_fwd_t(const BoundaryFwdArgs& a, cudaStream_t s) {
-  const unsigned rows8 = (unsigned)(((int64_t)a.T + 7) / 8);
-  if (a.d <= 256) boundary_fwd_kernel<TO, TX, 1, 1><<<rows8, 256, 0, s>>>(a);
-  else if (a.d <= 512) boundary_fwd_kernel<TO, TX, 1, 2><<<rows8, 256, 0, s>>>(a);
-  else if (a.d <= 1024) boundary_fwd_kernel<TO, TX, 2, 2><<<a.T, 64, 0, s>>>(a);
-  else if (a.d <= 2048) boundary_fwd_kernel<TO, TX, 4, 2><<<a.T, 128, 0, s>>>(a);
-  else if (a.d <= 4096) boundary_fwd_kernel<TO, TX, 8, 2><<<a.T, 256, 0, s>>>(a);
-  else boundary_fwd_kernel<TO, TX, 16, 2><<<a.T, 512, 0, s>>>(a);
+  const auto blocks = [&](int rows) { return (unsigned)(((int64_t)a.T + rows - 1) / rows); };
+  if (a.d <= 64) boundary_fwd_kernel<TO, TX, 1, 8, 1><<<blocks(32), 256, 0, s>>>(a);
+  else if (a.d <= 128) boundary_fwd_kernel<TO, TX, 1, 16, 1><<<blocks(16), 256, 0, s>>>(a);
+  else if (a.d <= 256) boundary_fwd_kernel<TO, TX, 1, 32, 1><<<blocks(8), 256, 0, s>>>(a);
+  else if (a.d <= 512) boundary_fwd_kernel<TO, TX, 1, 32, 2><<<blocks(8), 256, 0, s>>>(a);
+  else if (a.d <= 1024) boundary_fwd_kernel<TO, TX, 2, 32, 2><<<a.T, 64, 0, s>>>(a);
+  else if (a.d <= 2048) boundary_fwd_kernel<TO, TX, 4, 32, 2><<<a.T, 128, 0, s>>>(a);
+  else if (a.d <= 4096) boundary_fwd_kernel<TO, TX, 8, 32, 2><<<a.T, 256, 0, s>>>(a);
+  else boundary_fwd_kernel<TO, TX, 16, 32, 2><<<a.T, 512, 0, s>>>(a);
   return launch_status();
 }
 
@@ -327,40 +337,44 @@ constexpr int bwd_thread_bytes() {
   return 16 * VPL * (kParamPieces<WARPS> + (kAhead<WARPS> + 1) * kRowPieces<TO, TX>);
 }
 
-// Blocks an SM holds at once, by registers: 16 warps of one vector a thread, 8 of two.
+// Blocks an SM holds at once, by registers: 12 warps of one vector a thread, 8 of two
+// (16 of one, with spills, took 373 us against 249 at 200003 x 256).
 constexpr int bwd_blocks(int warps, int vpl) {
-  const int all = vpl == 1 ? 16 : 8, per = warps == 1 ? 4 : warps;
+  const int all = vpl == 1 ? 12 : 8, per = warps == 1 ? 4 : warps;
   return all / per > 0 ? all / per : 1;
 }
 
 // A team takes a contiguous run of rows (a user's segments are runs of one
-// group, so the group seldom changes): a warp for d <= 512, four to a block; above,
-// a block of WARPS warps. VPL vectors of eight columns a thread: two, so that a
+// group, so the group seldom changes): LANES lanes of a warp (8 for d <= 64, 16 for
+// d <= 128, 32 up to 512), four warps to a block; above, a block of WARPS warps. VPL vectors of eight columns a thread: two, so that a
 // thread has two independent chains and a row few exchanges (at 200003 x 512: 573
 // us with one vector and two warps a row). The parameter gradients gather in
 // registers while the group stays the same; then they go to the team's own slots
 // of the workspace (each thread its own columns: no atomics, and the same order of
 // sums in every run).
-template <typename TO, typename TX, int WARPS, int VPL>
+template <typename TO, typename TX, int WARPS, int LANES, int VPL>
 __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARPS, VPL))
     boundary_bwd_kernel(BoundaryBwdArgs a) {
   constexpr int AHEAD = kAhead<WARPS>, PP = kParamPieces<WARPS>;
   dependents_may_launch();
   extern __shared__ uint4 smem[];
   __shared__ float part[4 * WARPS];
-  Sums<WARPS> sums{part};
+  Sums<WARPS, LANES> sums{part};
   constexpr bool BLOCK = WARPS > 1;
-  const int tl = BLOCK ? threadIdx.x : threadIdx.x & 31;
-  const int64_t ti = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (ti >= a.teams) return;
+  const int tl = BLOCK ? threadIdx.x : threadIdx.x % LANES;
+  const int64_t ti = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (128 / LANES) + threadIdx.x / LANES;
+  if (LANES == 32 && ti >= a.teams) return;
   const int d = a.d;
-  constexpr int VSTEP = 8 * 32 * WARPS;  // columns between a thread's vectors
+  constexpr int VSTEP = 8 * LANES * WARPS;  // columns between a thread's vectors
   const int c0 = 8 * tl;
   bool on[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; ++j) on[j] = c0 + j * VSTEP < d;
   const int64_t t0 = ti * a.rows_per_team;
-  const int rows = (int)min((int64_t)a.rows_per_team, (int64_t)a.T - t0);
+  const int rows = ti < a.teams ? (int)min((int64_t)a.rows_per_team, (int64_t)a.T - t0) : 0;
+  // the warp's teams go through the loop together: one whose rows are done goes on
+  // with rows of zeros, which add nothing, and stores nothing
+  const int most = LANES == 32 ? rows : (int)__reduce_max_sync(0xffffffffu, (unsigned)rows);
   const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr, gate = a.gate != MTGR_GATE_NONE;
   const float inv_d = 1.0f / (float)d;
   float* slots = a.part + ti * a.G * kSlots * d + c0;
@@ -452,6 +466,8 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
             copy8(at + (2 * PO + 2 * PX) * step, step, static_cast<const __nv_bfloat16*>(a.dy) + t * d + c);
         }
       }
+    } else if (LANES < 32) {
+      for (int i = 0; i < VPL * RP; ++i) base[s * stage + i * step] = make_uint4(0u, 0u, 0u, 0u);
     }
     copy_commit();
   };
@@ -465,9 +481,10 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
 #pragma unroll
   for (int r = 0; r < AHEAD; ++r) copy_row(r, r);
   int g = rows > 0 ? clamp_group(a.gid, t0, a.G) : 0, s = 0;
-  for (int r = 0; r < rows; ++r) {
+  for (int r = 0; r < most; ++r) {
+    const bool live = LANES == 32 || r < rows;
     copy_row(r + AHEAD, s == 0 ? AHEAD : s - 1);  // stage (s + AHEAD) mod (AHEAD + 1)
-    const int g_next = r + 1 < rows ? clamp_group(a.gid, t0 + r + 1, a.G) : 0;
+    const int g_next = r + 1 < rows ? clamp_group(a.gid, t0 + r + 1, a.G) : g;
     if (g != g_run) {
       flush();
       g_run = g;
@@ -606,7 +623,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
 #pragma unroll
         for (int k = 0; k < 4; ++k) H[j][k] = add2(H[j][k], v[j][k]);
       }
-      if (on[j]) store_pairs(static_cast<TX*>(a.dx) + t * d + c, H[j]);
+      if (on[j] && live) store_pairs(static_cast<TX*>(a.dx) + t * d + c, H[j]);
       // sc becomes the gradient at p
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -627,7 +644,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
             v[j][k] = mul2(v[j][k], pair2(fmaf(y.x, 1.0f - s0, s0), fmaf(y.y, 1.0f - s1, s1)));
           }
         }
-        if (on[j]) {
+        if (on[j] && live) {
           store_pairs(static_cast<TO*>(a.du) + t * a.ld_du + c, v[j]);
           if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16) range_bad |= beyond_f16(v[j]);
         }
@@ -656,7 +673,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
     }
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-      if (on[j]) {
+      if (on[j] && live) {
         store_pairs(static_cast<TO*>(a.d_o) + t * a.ld_do + c0 + j * VSTEP, v[j]);
         if (sizeof(TO) == 2 && a.o_dtype == MTGR_F16) range_bad |= beyond_f16(v[j]);
       }
@@ -665,7 +682,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
     s = s == AHEAD ? 0 : s + 1;
   }
   flush();
-  if (tl == 0) a.seen[ti] = seen;
+  if (tl == 0 && ti < a.teams) a.seen[ti] = seen;
   if (range_bad) set_status(a.status, MTGR_ERR_RANGE);
 }
 
@@ -732,14 +749,15 @@ int32_t bwd_teams(int32_t T, int32_t d, int32_t G, int64_t resident) {
 // Warps of a row's team and vectors a thread.
 inline int bwd_warps(int d) { return d <= 512 ? 1 : (d <= 1024 ? 2 : (d <= 2048 ? 4 : (d <= 4096 ? 8 : 16))); }
 inline int bwd_vpl(int d) { return d <= 256 ? 1 : 2; }
+inline int bwd_lanes(int d) { return d <= 64 ? 8 : (d <= 128 ? 16 : 32); }
 
 // Most teams that any types of this width have resident at once.
 int64_t bwd_resident(int32_t d) {
   const int warps = bwd_warps(d);
-  return (int64_t)device_sm_count() * bwd_blocks(warps, bwd_vpl(d)) * (warps == 1 ? 4 : 1);
+  return (int64_t)device_sm_count() * bwd_blocks(warps, bwd_vpl(d)) * (warps == 1 ? 128 / bwd_lanes(d) : 1);
 }
 
-template <typename TO, typename TX, int WARPS, int VPL>
+template <typename TO, typename TX, int WARPS, int LANES, int VPL>
 int launch_bwd_w(BoundaryBwdArgs& a, cudaStream_t s) {
   constexpr int threads = WARPS == 1 ? 128 : 32 * WARPS;
   constexpr int bytes = threads * bwd_thread_bytes<TO, TX, WARPS, VPL>();
@@ -750,13 +768,14 @@ int launch_bwd_w(BoundaryBwdArgs& a, cudaStream_t s) {
   static_assert(by_smem >= 1, "shared memory of a block");
   constexpr int by_regs = bwd_blocks(WARPS, VPL);
   constexpr int blocks = by_regs < by_smem ? by_regs : by_smem;
-  a.teams = bwd_teams(a.T, a.d, a.G, (int64_t)device_sm_count() * blocks * (WARPS == 1 ? 4 : 1));
+  constexpr int per_block = WARPS == 1 ? 128 / LANES : 1;
+  a.teams = bwd_teams(a.T, a.d, a.G, (int64_t)device_sm_count() * blocks * per_block);
   a.rows_per_team = (a.T + a.teams - 1) / a.teams;
-  auto kern = boundary_bwd_kernel<TO, TX, WARPS, VPL>;
+  auto kern = boundary_bwd_kernel<TO, TX, WARPS, LANES, VPL>;
   if (bytes > 40 * 1024 &&  // 48 KB without asking, some of it static
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return MTGR_ERR_CUDA;
-  kern<<<WARPS == 1 ? (a.teams + 3) / 4 : a.teams, threads, bytes, s>>>(a);
+  kern<<<(a.teams + per_block - 1) / per_block, threads, bytes, s>>>(a);
   return launch_status();
 }
 
@@ -764,12 +783,14 @@ template <typename TO, typename TX>
 int launch_bwd_t(BoundaryBwdArgs& a, cudaStream_t s) {
   if (a.T > 0) {
     int rc = MTGR_OK;
-    if (a.d <= 256) rc = launch_bwd_w<TO, TX, 1, 1>(a, s);
-    else if (a.d <= 512) rc = launch_bwd_w<TO, TX, 1, 2>(a, s);
-    else if (a.d <= 1024) rc = launch_bwd_w<TO, TX, 2, 2>(a, s);
-    else if (a.d <= 2048) rc = launch_bwd_w<TO, TX, 4, 2>(a, s);
-    else if (a.d <= 4096) rc = launch_bwd_w<TO, TX, 8, 2>(a, s);
-    else rc = launch_bwd_w<TO, TX, 16, 2>(a, s);
+    if (a.d <= 64) rc = launch_bwd_w<TO, TX, 1, 8, 1>(a, s);
+    else if (a.d <= 128) rc = launch_bwd_w<TO, TX, 1, 16, 1>(a, s);
+    else if (a.d <= 256) rc = launch_bwd_w<TO, TX, 1, 32, 1>(a, s);
+    else if (a.d <= 512) rc = launch_bwd_w<TO, TX, 1, 32, 2>(a, s);
+    else if (a.d <= 1024) rc = launch_bwd_w<TO, TX, 2, 32, 2>(a, s);
+    else if (a.d <= 2048) rc = launch_bwd_w<TO, TX, 4, 32, 2>(a, s);
+    else if (a.d <= 4096) rc = launch_bwd_w<TO, TX, 8, 32, 2>(a, s);
+    else rc = launch_bwd_w<TO, TX, 16, 32, 2>(a, s);
     if (rc != MTGR_OK) return rc;
   }
   const int64_t n = (int64_t)a.G * kSlots * a.d;

@@ -122,7 +122,7 @@ def oracle_args(r):
 
 
 # ------------------------------------------------------- boundary, forward --
-SHAPES = [(1, 8), (3, 64), (5, 200), (33, 256), (9, 264), (17, 512), (4, 1000), (6, 1024), (3, 1032), (2, 2048), (2, 5000),
+SHAPES = [(1, 8), (3, 64), (70, 40), (37, 72), (50, 128), (5, 200), (33, 256), (9, 264), (17, 512), (4, 1000), (6, 1024), (3, 1032), (2, 2048), (2, 5000),
           (2, 8192)]
 
 
@@ -239,7 +239,7 @@ def upstream(T, d, stream=torch.float32, y=torch.bfloat16, seed=5):
     return torch.randn(T, d, generator=g).to(stream).cuda(), torch.randn(T, d, generator=g).to(y).cuda()
 
 
-@pytest.mark.parametrize("T,d", SHAPES + [(300, 64), (1500, 256), (700, 512)])
+@pytest.mark.parametrize("T,d", SHAPES + [(300, 64), (1003, 120), (1500, 256), (700, 512)])
 @pytest.mark.parametrize("gate", GATES)
 def test_boundary_backward_shapes(T, d, gate):
     dev, r = case(T, d, gate=gate)
@@ -258,7 +258,7 @@ def test_boundary_backward_types(branch, stream, y):
 @pytest.mark.parametrize("post,scale,pre", [(False, True, True), (True, False, True), (True, True, False),
                                             (False, False, False), (False, False, True)])
 @pytest.mark.parametrize("gate", GATES)
-@pytest.mark.parametrize("d", [200, 264])
+@pytest.mark.parametrize("d", [56, 200, 264])
 def test_boundary_backward_parts_left_out(post, scale, pre, gate, d):
     dev, r = case(21, d, gate=gate, post=post, scale=scale, pre=pre)
     dh, dy = upstream(21, d)
@@ -267,12 +267,13 @@ def test_boundary_backward_parts_left_out(post, scale, pre, gate, d):
         check_backward(dev, r, gate, None, dy)
 
 
+@pytest.mark.parametrize("d", [64, 104, 264])
 @pytest.mark.parametrize("G", [1, 4, 32])
-def test_boundary_backward_groups_in_any_order(G):
+def test_boundary_backward_groups_in_any_order(G, d):
     # the group changes at nearly every row: every change adds to the team's slots
     gid = np.random.default_rng(G).integers(0, G, 400)
-    dev, r = case(400, 264, G=G, gid=gid)
-    check_backward(dev, r, "linear", *upstream(400, 264))
+    dev, r = case(400, d, G=G, gid=gid)
+    check_backward(dev, r, "linear", *upstream(400, d))
 
 
 def test_boundary_backward_same_bits_every_time():
