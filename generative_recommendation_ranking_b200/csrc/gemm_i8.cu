@@ -10,11 +10,18 @@
 // Design: persistent warp-specialised kernel as for the bf16 product: TMA loads of
 // 128-byte k-blocks (128-byte swizzle) through an mbarrier ring, one thread
 // issuing tcgen05.mma kind::i8 (K = 32 per instruction, twice the bf16 rate), and
-// epilogue warps that drain a double-buffered accumulator, stage 32 x 32 blocks in
-// swizzled shared memory and leave them by TMA stores.
+// epilogue warps that drain a double-buffered accumulator, stage blocks of 32 rows x
+// 128 bytes in swizzled shared memory and leave them by TMA stores.
 //   CG = 2: CTA pairs, 256 x 256 tiles (an SM reads its 128 rows of a and half of
 //           the 256 columns of b): many rows.
 //   CG = 1: one CTA, 128 x 64 tiles, so that a few hundred rows spread over the SMs.
+//   KEEP_B (pairs, k <= 512): a pair stays in its 256 columns and keeps their b in
+//           shared memory, which halves what L2 hands to the SMs.
+// Measured on one B200, bursts of 20: 8192^3 at 2.9-3.1 P op/s, where the operands'
+// way out of L2 (about 12 TB/s) bounds it (without b's loads 3.7); 131075 x 2048 x 512
+// to f16 146 us (b reloaded: 152), its output's way to DRAM beside the epilogue (no
+// stores: 105, no epilogue arithmetic: 139); to fp32 196 us, 5.8 TB/s. In a long run
+// at the power limit the f16 one takes 170 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -26,6 +33,7 @@
 #include "common.cuh"
 #include "ops.h"
 #include "ptx.cuh"
+#include "rowvec.cuh"
 #include "tmap.h"
 
 namespace mtgr {
@@ -35,6 +43,7 @@ namespace {
 constexpr int BM = 128;   // rows of a per CTA
 constexpr int BK = 128;   // bytes of k per stage: one swizzle row
 constexpr int A_BYTES = BM * BK;
+constexpr int kKeepK = 512;  // longest k whose tile of b stays in shared memory
 
 template <int CG>
 struct Shape {
@@ -50,7 +59,7 @@ struct Shape {
 // (kWarps / 4)th share of the columns, in staging blocks of 32 rows x 128 bytes: whole
 // lines for the TMA store. Sixteen warps for the 16-bit outputs of the pair form,
 // whose main loop is short at K = 512; eight for its fp32 outputs.
-template <int OUT, int CG>
+template <int OUT, int CG, bool KEEP_B>
 struct Epi {
   static constexpr int kWarps = CG == 2 ? (OUT != MTGR_F32 ? 16 : 8) : 4;
   static constexpr int kThreads = 64 + 32 * kWarps;
@@ -58,8 +67,9 @@ struct Epi {
   static constexpr int kBlocks = (Shape<CG>::kBN / kCols) / (kWarps / 4);  // a warp's blocks per tile
   static constexpr int kBufs = kBlocks > 1 ? 2 : 1;
   static constexpr int kStg = 4096;
-  static constexpr int kStages = CG == 1 ? 6 : 5;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * Shape<CG>::kStageBytes +
+  static constexpr int kStages = KEEP_B || CG == 1 ? 6 : 5;
+  static constexpr int kBBlocks = KEEP_B ? kKeepK / BK : kStages;  // blocks of b in shared memory
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * A_BYTES + (size_t)kBBlocks * Shape<CG>::kBBytes +
                                   (size_t)kWarps * kBufs * kStg + 256;
   static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
@@ -102,23 +112,6 @@ __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t
 // 16-byte chunk c of row r of a staging block (128-byte rows, 128-byte swizzle)
 __device__ __forceinline__ uint32_t stg_off(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// Two fp32 values in one 64-bit register pair: sm_100 multiplies and adds pairs in
-// one instruction, which halves the epilogue's fp32 work.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // 32 columns' values of a per-column array (16-byte aligned), the same for every
 // lane; columns past N (N % 8 == 0) are 0. FULL: there are none.
 template <bool FULL>
@@ -143,13 +136,13 @@ __device__ __forceinline__ void epilogue_cols(const Args& a, int col0, float sa,
   reg_fence(acc);
   loaded();
   float v[32];
-  const uint64_t sa2 = pair(sa, sa);
+  const f2 sa2 = both(sa);
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    const float2 lo = unpair(mul2(pair(__int2float_rn((int)acc[4 * c]), __int2float_rn((int)acc[4 * c + 1])),
-                                  mul2(sa2, pair(sb[c].x, sb[c].y))));
-    const float2 hi = unpair(mul2(pair(__int2float_rn((int)acc[4 * c + 2]), __int2float_rn((int)acc[4 * c + 3])),
-                                  mul2(sa2, pair(sb[c].z, sb[c].w))));
+    const float2 lo = unpair2(mul2(pair2(__int2float_rn((int)acc[4 * c]), __int2float_rn((int)acc[4 * c + 1])),
+                                  mul2(sa2, pair2(sb[c].x, sb[c].y))));
+    const float2 hi = unpair2(mul2(pair2(__int2float_rn((int)acc[4 * c + 2]), __int2float_rn((int)acc[4 * c + 3])),
+                                  mul2(sa2, pair2(sb[c].z, sb[c].w))));
     v[4 * c] = lo.x; v[4 * c + 1] = lo.y; v[4 * c + 2] = hi.x; v[4 * c + 3] = hi.y;
   }
   if (a.bias != nullptr) {
@@ -206,34 +199,52 @@ __device__ __forceinline__ void epilogue_cols(const Args& a, int col0, float sa,
   }
 }
 
-template <int EPI, int OUT, int CG>
-__global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
+template <int EPI, int OUT, int CG, bool KEEP_B>
+__global__ void __launch_bounds__(Epi<OUT, CG, KEEP_B>::kThreads, 1)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmO, Args args) {
   using S = Shape<CG>;
-  using E = Epi<OUT, CG>;
+  using E = Epi<OUT, CG, KEEP_B>;
   constexpr int NST = E::kStages, BN = S::kBN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + NST * A_BYTES;
-  uint8_t* sStg = sB + NST * S::kBBytes;
+  uint8_t* sStg = sB + E::kBBlocks * S::kBBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sStg + E::kWarps * E::kBufs * E::kStg);
   uint64_t* full = bars;
   uint64_t* empty = bars + NST;
   uint64_t* acc_full = bars + 2 * NST;
   uint64_t* acc_empty = bars + 2 * NST + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 4);
+  uint64_t* b_full = bars + 2 * NST + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 5);
 
   const int warp = warp_id(), lane = lane_id();
   const int M = args.M, N = args.N;
   const int n_tiles = (N + BN - 1) / BN;
-  const int num_tiles = ((M + S::kTileM - 1) / S::kTileM) * n_tiles;
+  const int m_tiles = (M + S::kTileM - 1) / S::kTileM;
   const int kblocks = (args.K + BK - 1) / BK;  // a ragged last block is zero-filled by the loads
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
-  const int tile0 = CG == 2 ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-  const int tstride = CG == 2 ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  const int unit = CG == 2 ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int units = CG == 2 ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  // The i-th tile of this block or pair; false behind the last. KEEP_B: it stays in
+  // its columns (units >= n_tiles), whose b stays in shared memory, and takes every
+  // so many-th row tile, as many as every other column's pairs, so that a row's tiles
+  // are written at about the same time; else all tiles in turn, columns first.
+  const auto tile_at = [&](int i, int& mb, int& nb) {
+    if constexpr (KEEP_B) {
+      const int per = units / n_tiles;  // pairs a column of tiles; the rest of the pairs have none
+      nb = unit % n_tiles;
+      mb = unit / n_tiles + i * per;
+      return unit < per * n_tiles && mb < m_tiles;
+    } else {
+      const int t = unit + i * units;
+      mb = t / n_tiles;
+      nb = t - mb * n_tiles;
+      return mb < m_tiles;
+    }
+  };
 
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
@@ -247,6 +258,7 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
       mbar_init(&acc_full[a], 1);
       mbar_init(&acc_empty[a], CG * E::kWarps);  // the pair's epilogue warps, on the leader's barrier
     }
+    mbar_init(b_full, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -270,8 +282,14 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      for (int tile = tile0; tile < num_tiles && !timed_out; tile += tstride) {
-        const int mb = tile / n_tiles, nb = tile % n_tiles;
+      int mb, nb;
+      if (KEEP_B && tile_at(0, mb, nb)) {
+        if (rank == 0) mbar_arrive_expect_tx(b_full, 2 * kblocks * S::kBBytes);
+        const uint32_t fb = mapa_shared(b_full, 0);
+        for (int kb = 0; kb < kblocks; ++kb)
+          tma_load_2d_cg2(&tmB, fb, sB + kb * S::kBBytes, kb * BK, nb * BN + (int)rank * S::kBRows);
+      }
+      for (int i = 0; tile_at(i, mb, nb) && !timed_out; ++i) {
         for (int kb = 0; kb < kblocks; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1)) { timed_out = true; break; }
           uint8_t* da = sA + stage * A_BYTES;
@@ -280,10 +298,10 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
           if constexpr (CG == 2) {
             // both CTAs' halves complete on the leader's barrier, which the
             // leader arms for the bytes of both
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (KEEP_B ? A_BYTES : S::kStageBytes));
             const uint32_t fb = mapa_shared(&full[stage], 0);
             tma_load_2d_cg2(&tmA, fb, da, kb * BK, ya);
-            tma_load_2d_cg2(&tmB, fb, db, kb * BK, yb);
+            if (!KEEP_B) tma_load_2d_cg2(&tmB, fb, db, kb * BK, yb);
           } else {
             mbar_arrive_expect_tx(&full[stage], S::kStageBytes);
             tma_load_2d(&tmA, &full[stage], da, kb * BK, ya);
@@ -298,7 +316,9 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
       constexpr uint32_t idesc = idesc_i8(S::kTileM, BN);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      for (int tile = tile0; tile < num_tiles && !timed_out; tile += tstride) {
+      int mb, nb;
+      if (KEEP_B && tile_at(0, mb, nb)) timed_out = !mbar_wait(b_full, 0);
+      for (int i = 0; tile_at(i, mb, nb) && !timed_out; ++i) {
         if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1)) { timed_out = true; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
@@ -306,7 +326,7 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
           if (!mbar_wait(&full[stage], phase)) { timed_out = true; break; }
           tc_fence_after();
           const uint32_t a_addr = smem_u32(sA + stage * A_BYTES);
-          const uint32_t b_addr = smem_u32(sB + stage * S::kBBytes);
+          const uint32_t b_addr = smem_u32(sB + (KEEP_B ? kb : stage) * S::kBBytes);
 #pragma unroll
           for (int k = 0; k < BK / 32; ++k)
             mma_i8<CG>(d_tmem, sdesc_sw128(a_addr + 32 * k, 16, 1024), sdesc_sw128(b_addr + 32 * k, 16, 1024),
@@ -338,13 +358,14 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
     constexpr int RB = EPI == MTGR_EPI_RESID ? 2 : 1;
     static_assert(EPI != MTGR_EPI_RESID || NB % RB == 0, "a block's ring slot is its index mod RB");
     float4 rs[RB][8];
-    int lt = tile0, lc = 0;  // the next block to load
+    int li = 0, lc = 0;  // the next block to load
     auto load_next = [&](float4 (&z)[8]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (lt < num_tiles) {
-        const int m = (lt / n_tiles) * S::kTileM + (int)rank * BM + quarter * 32 + lane;
-        const int col = (lt % n_tiles) * BN + (grp * NB + lc) * 32;
+      int mb, nb;
+      if (tile_at(li, mb, nb)) {
+        const int m = mb * S::kTileM + (int)rank * BM + quarter * 32 + lane;
+        const int col = nb * BN + (grp * NB + lc) * 32;
         if (m < M) {
           const float4* p = reinterpret_cast<const float4*>(args.resid + (size_t)m * N + col);
 #pragma unroll
@@ -352,14 +373,14 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
             if (col + 4 * i < N) z[i] = __ldg(p + i);
         }
       }
-      if (++lc == NB) { lc = 0; lt += tstride; }
+      if (++lc == NB) { lc = 0; ++li; }
     };
     if constexpr (EPI == MTGR_EPI_RESID) {
 #pragma unroll
       for (int sl = 0; sl < RB; ++sl) load_next(rs[sl]);
     }
-    for (int tile = tile0; tile < num_tiles; tile += tstride) {
-      const int mb = tile / n_tiles, nb = tile % n_tiles;
+    int mb, nb;
+    for (int i = 0; tile_at(i, mb, nb); ++i) {
       const int row0 = mb * S::kTileM + (int)rank * BM + quarter * 32;
       const float sa = row0 + lane < M ? __ldg(args.sa + row0 + lane) : 0.f;
       const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase));
@@ -433,11 +454,11 @@ __global__ void __launch_bounds__(Epi<OUT, CG>::kThreads, 1)
 
 constexpr int kMaxDevices = 64;
 
-template <int EPI, int OUT, int CG>
+template <int EPI, int OUT, int CG, bool KEEP_B>
 int launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const Args& args,
              cudaStream_t s, bool dependent) {
-  using E = Epi<OUT, CG>;
-  auto kern = gemm_i8_kernel<EPI, OUT, CG>;
+  using E = Epi<OUT, CG, KEEP_B>;
+  auto kern = gemm_i8_kernel<EPI, OUT, CG, KEEP_B>;
   // per device: blocks (pairs) resident at once; 0 until the first launch there
   static std::atomic<int> resident[kMaxDevices];
   int dev = 0;
@@ -470,6 +491,8 @@ int launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to
   }
   const int64_t tiles = (((int64_t)args.M + BM * CG - 1) / (BM * CG)) *
                         ((args.N + Shape<CG>::kBN - 1) / Shape<CG>::kBN);
+  if (KEEP_B && units < (args.N + Shape<CG>::kBN - 1) / Shape<CG>::kBN)  // a pair per column at least
+    return launch_t<EPI, OUT, CG, false>(ta, tb, to, args, s, dependent);
   if (tiles > 0x3fffffff) return MTGR_ERR_UNSUPPORTED;  // the kernel counts tiles in 32 bits
   cfg.gridDim = dim3((unsigned)(CG * (tiles < units ? tiles : units)));
   cfg.numAttrs = dependent ? 2 : 1;
@@ -494,8 +517,12 @@ int launch_cg(int M, int N, int K, const int8_t* a, const int8_t* b, int epi, in
            : make_tmap_2d(&to, out, CU_TENSOR_MAP_DATA_TYPE_UINT16, (uint64_t)N, (uint64_t)M,
                           (uint64_t)N * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc != MTGR_OK) return rc;
+  // b's tile stays where k is short and every pair has several row tiles
+  const bool keep = CG == 2 && K <= kKeepK && (N + S::kBN - 1) / S::kBN <= device_sm_count() / 8;
 #define MTGR_FORM(E, O) \
-  if (epi == E && out_dtype == O) return launch_t<E, O, CG>(ta, tb, to, args, s, dependent)
+  if (epi == E && out_dtype == O)                                                     \
+    return keep ? launch_t<E, O, CG, CG == 2>(ta, tb, to, args, s, dependent)          \
+                : launch_t<E, O, CG, false>(ta, tb, to, args, s, dependent)
   MTGR_FORM(MTGR_EPI_NONE, MTGR_F16);
   MTGR_FORM(MTGR_EPI_NONE, MTGR_BF16);
   MTGR_FORM(MTGR_EPI_NONE, MTGR_F32);
