@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) boundary_fwd_ke
   }
   if (a.pre_gamma == nullptr) return;
   const float rstd_h = centre();
-  uint32_t m = 0u;
+  float m = 0.f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     const int c = c0 + j * VSTEP;
@@ -251,26 +251,17 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) boundary_fwd_ke
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 f = unpair2(h[j][k]);
-        m = max(m, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
+        m = max_nan(m, max_nan(fabsf(f.x), fabsf(f.y)));
       }
     }
   }
   if (a.y_dtype != MTGR_I8) return;
-  const RowScale rs = row_scale(sums.max_bits(m));
+  const RowScale rs = row_scale(sums.max_bits(__float_as_uint(m)));
   if (tl == 0 && d > 0) a.y_scale[t] = rs.s;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
     const int c = c0 + j * VSTEP;
-    if (c < d) {
-      float y[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = unpair2(h[j][k]);
-        y[2 * k] = f.x;
-        y[2 * k + 1] = f.y;
-      }
-      *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.y) + t * d + c) = quant8(y, rs);
-    }
+    if (c < d) *reinterpret_cast<uint2*>(static_cast<int8_t*>(a.y) + t * d + c) = quant8(h[j], rs);
   }
 }
 

@@ -64,23 +64,20 @@ __device__ __forceinline__ float take_row(const FewArgs& a, int r, uint8_t* to, 
     s = a.sa[r];
   } else {
     const TX* from = static_cast<const TX*>(a.x) + (int64_t)r * a.ld_x;
-    uint32_t mx = 0u;
+    float mx = 0.f;
 #pragma unroll 4
     for (int vi = lane; vi < nv; vi += 32) {
       Vec8<TX> w;
       w.load(from + 8 * vi);
-      float v[8];
-      w.unpack(v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mx = max(mx, __float_as_uint(fabsf(v[e])));
+      mx = max_nan(mx, max_abs8(w));
     }
-    const RowScale rs = row_scale(__reduce_max_sync(0xffffffffu, mx));
+    const RowScale rs = row_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
 #pragma unroll 4
     for (int vi = lane; vi < nv; vi += 32) {
       Vec8<TX> w;
       w.load(from + 8 * vi);
-      float v[8];
-      w.unpack(v);
+      f2 v[4];
+      w.pairs(v);
       *reinterpret_cast<uint2*>(to + 8 * vi) = quant8(v, rs);
     }
     s = rs.s;

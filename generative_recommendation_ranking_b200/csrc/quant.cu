@@ -35,23 +35,18 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
     const int vi = tl + THREADS * k;
     if (vi < nv) r[k].load(x + m * ld_x + 8 * vi);
   }
-  uint32_t mx = 0u;
+  float mx = 0.f;
 #pragma unroll
   for (int k = 0; k < VPL; ++k)
-    if (tl + THREADS * k < nv) {
-      float v[8];
-      r[k].unpack(v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mx = max(mx, __float_as_uint(fabsf(v[e])));
-    }
-  const RowScale rs = row_scale(team.max_bits(mx));
+    if (tl + THREADS * k < nv) mx = max_nan(mx, max_abs8(r[k]));
+  const RowScale rs = row_scale(team.max_bits(__float_as_uint(mx)));
   if (tl == 0) scale[m] = rs.s;
 #pragma unroll
   for (int k = 0; k < VPL; ++k) {
     const int vi = tl + THREADS * k;
     if (vi < nv) {
-      float v[8];
-      r[k].unpack(v);
+      f2 v[4];
+      r[k].pairs(v);
       *reinterpret_cast<uint2*>(q + m * K + 8 * vi) = quant8(v, rs);
     }
   }
@@ -64,10 +59,10 @@ int launch_t(int32_t M, int32_t K, const void* xv, int64_t ld_x, int8_t* q, floa
   if (K <= 256) quantize_rows_kernel<T, 32, 1><<<warps, 256, 0, s>>>(M, K, x, ld_x, q, scale);
   else if (K <= 512) quantize_rows_kernel<T, 32, 2><<<warps, 256, 0, s>>>(M, K, x, ld_x, q, scale);
   else if (K <= 1024) quantize_rows_kernel<T, 32, 4><<<warps, 256, 0, s>>>(M, K, x, ld_x, q, scale);
-  else if (K <= 2048) quantize_rows_kernel<T, 128, 2><<<M, 128, 0, s>>>(M, K, x, ld_x, q, scale);
-  else if (K <= 4096) quantize_rows_kernel<T, 256, 2><<<M, 256, 0, s>>>(M, K, x, ld_x, q, scale);
-  else if (K <= 8192) quantize_rows_kernel<T, 256, 4><<<M, 256, 0, s>>>(M, K, x, ld_x, q, scale);
-  else quantize_rows_kernel<T, 1024, 4><<<M, 1024, 0, s>>>(M, K, x, ld_x, q, scale);
+  else if (K <= 2048) quantize_rows_kernel<T, 32, 8><<<warps, 256, 0, s>>>(M, K, x, ld_x, q, scale);
+  else if (K <= 4096) quantize_rows_kernel<T, 64, 8><<<M, 64, 0, s>>>(M, K, x, ld_x, q, scale);
+  else if (K <= 8192) quantize_rows_kernel<T, 128, 8><<<M, 128, 0, s>>>(M, K, x, ld_x, q, scale);
+  else quantize_rows_kernel<T, 512, 8><<<M, 512, 0, s>>>(M, K, x, ld_x, q, scale);
   return launch_status();
 }
 

@@ -24,6 +24,7 @@ struct Vec8<float> {
     b = *(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const;
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -35,6 +36,7 @@ struct Vec8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const;
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -50,6 +52,7 @@ struct Vec8<__half> {
   uint4 a;
   __device__ __forceinline__ void load(const __half* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const;
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -145,6 +148,17 @@ __device__ __forceinline__ void to_pairs(const uint4& a, const uint4&, f2 (&v)[4
     v[k] = pair2(f.x, f.y);
   }
 }
+__device__ __forceinline__ void Vec8<float>::pairs(uint64_t (&v)[4]) const {
+  v[0] = pair2(a.x, a.y);
+  v[1] = pair2(a.z, a.w);
+  v[2] = pair2(b.x, b.y);
+  v[3] = pair2(b.z, b.w);
+}
+__device__ __forceinline__ void Vec8<__nv_bfloat16>::pairs(uint64_t (&v)[4]) const {
+  to_pairs(a, a, v, __nv_bfloat16());
+}
+__device__ __forceinline__ void Vec8<__half>::pairs(uint64_t (&v)[4]) const { to_pairs(a, a, v, __half()); }
+
 template <typename T>
 __device__ __forceinline__ void store_pairs(T* p, const f2 (&v)[4]) {
   float o[8];
@@ -255,21 +269,25 @@ __device__ __forceinline__ RowScale row_scale(uint32_t max_abs_bits) {
 // the remainder v - q s is exact in fp32 (q has at most 7 bits and the
 // remainder is a multiple of an ulp of s or of v not above s/2 by more than a
 // few ulp), so it tells: beyond s / 2, or at s / 2 with an odd q, q moves by one.
-__device__ __forceinline__ uint2 quant8(const float (&v)[8], const RowScale& r) {
+__device__ __forceinline__ uint2 quant8(const f2 (&v)[4], const RowScale& r) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are the rounded integer
   const float half = 0.5f * r.s;
   uint32_t t[8];
   float far = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float m = fmaf(v[e], r.inv, kMagic);
-    t[e] = __float_as_uint(m);
-    far = fmaxf(far, fabsf(fmaf(-(m - kMagic), r.s, v[e])));
+  for (int k = 0; k < 4; ++k) {
+    const f2 m = fma2(v[k], both(r.inv), both(kMagic));
+    const float2 rem = unpair2(fma2(add2(m, both(-kMagic)), both(-r.s), v[k]));
+    far = fmaxf(far, fmaxf(fabsf(rem.x), fabsf(rem.y)));
+    const float2 q = unpair2(m);
+    t[2 * k] = __float_as_uint(q.x);
+    t[2 * k + 1] = __float_as_uint(q.y);
   }
   if (far >= half) {  // rare; false for s = NaN
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float rem = fmaf(-(__uint_as_float(t[e]) - kMagic), r.s, v[e]);
+      const float2 p = unpair2(v[e >> 1]);
+      const float rem = fmaf(-(__uint_as_float(t[e]) - kMagic), r.s, e & 1 ? p.y : p.x);
       const float ar = fabsf(rem);
       if (ar > half || (ar == half && (t[e] & 1u))) t[e] += rem > 0.f ? 1u : 0xffffffffu;
     }
@@ -282,6 +300,29 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], const RowScale& r) 
   o.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
   o.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
   return o;
+}
+
+// Largest magnitude of eight values as loaded, as fp32 bits; a NaN stays one, above
+// every number.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_abs8(const Vec8<float>& r) {
+  const float a = max_nan(max_nan(fabsf(r.a.x), fabsf(r.a.y)), max_nan(fabsf(r.a.z), fabsf(r.a.w)));
+  const float b = max_nan(max_nan(fabsf(r.b.x), fabsf(r.b.y)), max_nan(fabsf(r.b.z), fabsf(r.b.w)));
+  return max_nan(a, b);
+}
+__device__ __forceinline__ float max_abs8(const Vec8<__nv_bfloat16>& r) {
+  const auto h = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h(r.a.x), h(r.a.y)), __hmax2_nan(h(r.a.z), h(r.a.w)));
+  return max_nan(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float max_abs8(const Vec8<__half>& r) {
+  const auto h = [](uint32_t w) { return __habs2(*reinterpret_cast<const __half2*>(&w)); };
+  const __half2 m = __hmax2_nan(__hmax2_nan(h(r.a.x), h(r.a.y)), __hmax2_nan(h(r.a.z), h(r.a.w)));
+  return max_nan(__low2float(m), __high2float(m));
 }
 
 }  // namespace mtgr
