@@ -145,16 +145,19 @@ struct Sums {
 
 // ---------------------------------------------------------------- forward --
 // A row per team: LANES lanes of a warp (8 for d <= 64, 16 for d <= 128, 32 up to 512),
-// or a block of WARPS warps, VPL vectors of eight columns a thread; a row is read once and stays in registers
-// through both norms. Two vectors a thread: at 65537 x 1024 with int8 y, one warp a
-// row with four took 226 us (16 warps an SM, by registers).
+// or a block of WARPS warps, VPL vectors of eight columns a thread; a row is read once
+// and stays in registers through both norms. Two vectors a thread (at 65537 x 1024 with int8 y, one warp a
+// row with four took 226 us, two warps with two 171), small blocks, so that rows of
+// different blocks are in different steps (200003 x 512: 261 us in blocks of eight
+// rows, 237 of two), and 28 warps an SM by registers.
 template <typename TO, typename TX, int WARPS, int LANES, int VPL>
-__global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) boundary_fwd_kernel(BoundaryFwdArgs a) {
+__global__ void __launch_bounds__(WARPS == 1 ? 64 : 32 * WARPS, VPL == 2 ? 28 / (WARPS < 2 ? 2 : WARPS) : 1)
+    boundary_fwd_kernel(BoundaryFwdArgs a) {
   constexpr bool BLOCK = WARPS > 1;
   __shared__ float part[BLOCK ? 4 * WARPS : 1];
   Sums<WARPS, LANES> sums{part};
   const int tl = BLOCK ? threadIdx.x : threadIdx.x % LANES;
-  const int64_t t = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t t = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * (64 / LANES) + threadIdx.x / LANES;
   if (LANES == 32 && t >= a.T) return;
   const int d = t < a.T ? a.d : 0;  // a team without a row has no columns, but goes along
   constexpr int VSTEP = 8 * LANES * WARPS;  // columns between a thread's vectors
@@ -268,10 +271,10 @@ __global__ void __launch_bounds__(WARPS == 1 ? 256 : 32 * WARPS) boundary_fwd_ke
 template <typename TO, typename TX>
 int launch_fwd_t(const BoundaryFwdArgs& a, cudaStream_t s) {
   const auto blocks = [&](int rows) { return (unsigned)(((int64_t)a.T + rows - 1) / rows); };
-  if (a.d <= 64) boundary_fwd_kernel<TO, TX, 1, 8, 1><<<blocks(32), 256, 0, s>>>(a);
-  else if (a.d <= 128) boundary_fwd_kernel<TO, TX, 1, 16, 1><<<blocks(16), 256, 0, s>>>(a);
-  else if (a.d <= 256) boundary_fwd_kernel<TO, TX, 1, 32, 1><<<blocks(8), 256, 0, s>>>(a);
-  else if (a.d <= 512) boundary_fwd_kernel<TO, TX, 1, 32, 2><<<blocks(8), 256, 0, s>>>(a);
+  if (a.d <= 64) boundary_fwd_kernel<TO, TX, 1, 8, 1><<<blocks(8), 64, 0, s>>>(a);
+  else if (a.d <= 128) boundary_fwd_kernel<TO, TX, 1, 16, 1><<<blocks(4), 64, 0, s>>>(a);
+  else if (a.d <= 256) boundary_fwd_kernel<TO, TX, 1, 32, 1><<<blocks(2), 64, 0, s>>>(a);
+  else if (a.d <= 512) boundary_fwd_kernel<TO, TX, 1, 32, 2><<<blocks(2), 64, 0, s>>>(a);
   else if (a.d <= 1024) boundary_fwd_kernel<TO, TX, 2, 32, 2><<<a.T, 64, 0, s>>>(a);
   else if (a.d <= 2048) boundary_fwd_kernel<TO, TX, 4, 32, 2><<<a.T, 128, 0, s>>>(a);
   else if (a.d <= 4096) boundary_fwd_kernel<TO, TX, 8, 32, 2><<<a.T, 256, 0, s>>>(a);
