@@ -23,29 +23,34 @@ namespace mtgr {
 
 namespace {
 
-constexpr int kTable = 96;            // tensors per launch
+// Tensors per launch: a launch costs more the more it carries (2.9 against 0.5 KB of
+// parameters), so small sets go in a small table.
+constexpr int kTable = 96, kSmallTable = 16;
 constexpr int64_t kChunk = 16384;     // elements a block takes at a time
 
+template <int N>
 struct Table {
-  const void* g[kTable];
-  void* out[kTable];
-  int64_t n[kTable];
-  int32_t chunk0[kTable + 1];  // first chunk of each tensor
-  uint8_t dtype[kTable];       // in | out << 4
+  const void* g[N];
+  void* out[N];
+  int64_t n[N];
+  int32_t chunk0[N + 1];  // first chunk of each tensor
+  uint8_t dtype[N];       // in | out << 4
   int32_t count;
 };
 
 // The tensor of a chunk: the last one whose first chunk is not behind it. All
 // lanes look at once, by generic loads: a search by halves costs seven misses of the
 // constant cache in a row, most of a small set's time.
-__device__ __forceinline__ int find_tensor(const Table& t, int chunk) {
+template <int N>
+__device__ __forceinline__ int find_tensor(const Table<N>& t, int chunk) {
+  constexpr int R = (N + 31) / 32;
   const int lane = threadIdx.x & 31;
-  int n = 0, first[kTable / 32];
+  int n = 0, first[R];
 #pragma unroll
-  for (int i = 0; i < kTable / 32; ++i)
-    asm volatile("ld.s32 %0, [%1];" : "=r"(first[i]) : "l"(&t.chunk0[lane + 32 * i]));
+  for (int i = 0; i < R; ++i)
+    asm volatile("ld.s32 %0, [%1];" : "=r"(first[i]) : "l"(&t.chunk0[min(lane + 32 * i, N)]));
 #pragma unroll
-  for (int i = 0; i < kTable / 32; ++i)
+  for (int i = 0; i < R; ++i)
     n += __popc(__ballot_sync(0xffffffffu, lane + 32 * i < t.count && first[i] <= chunk));
   return n - 1;
 }
@@ -101,7 +106,8 @@ __device__ __forceinline__ double block_sum(double s) {
   return s;
 }
 
-__global__ void __launch_bounds__(256) grad_sum_kernel(const __grid_constant__ Table t, double* part) {
+template <int N>
+__global__ void __launch_bounds__(256) grad_sum_kernel(const __grid_constant__ Table<N> t, double* part) {
   double s = 0.0;
   const int chunks = t.chunk0[t.count];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -154,7 +160,8 @@ __device__ __forceinline__ void scale_chunk(const void* gv, void* ov, int64_t e0
 }
 
 // parts: the sums of all launches of the first kernel. scale == 0: the norm only.
-__global__ void __launch_bounds__(256) grad_scale_kernel(const __grid_constant__ Table t, const double* part,
+template <int N>
+__global__ void __launch_bounds__(256) grad_scale_kernel(const __grid_constant__ Table<N> t, const double* part,
                                                          int32_t parts, float max_norm, float inv_scale,
                                                          int32_t scale, float* norm_out, int32_t* status) {
   double s = 0.0;
@@ -194,7 +201,8 @@ int grid_of(int64_t chunks) {
 int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
 
 // Tensors [first, last) of one launch as a table; empty tensors take no chunk.
-void fill(Table& t, const mtgr_grad_tensor* g, int first, int last) {
+template <int N>
+void fill(Table<N>& t, const mtgr_grad_tensor* g, int first, int last) {
   int64_t c = 0;
   for (int i = first; i < last; ++i) {
     t.g[i - first] = g[i].g;
@@ -206,6 +214,40 @@ void fill(Table& t, const mtgr_grad_tensor* g, int first, int last) {
   }
   t.count = last - first;
   t.chunk0[t.count] = (int32_t)c;
+}
+
+template <int N>
+int launch_n(const mtgr_grad_tensor* g, int32_t n, float max_norm, float inv_scale, float* norm,
+                     void* ws, int32_t* status, cudaStream_t s) {
+  double* part = static_cast<double*>(ws);
+  Table<N> t;
+  t.count = 0;
+  t.chunk0[0] = 0;
+  int32_t parts = 0;
+  bool scale = false;
+  for (int32_t i = 0; i < n; i += N) {
+    fill(t, g, i, n < i + N ? n : i + N);
+    for (int k = 0; k < t.count; ++k) scale = scale || t.out[k] != nullptr;
+    const int grid = grid_of(t.chunk0[t.count]);
+    grad_sum_kernel<N><<<grid, 256, 0, s>>>(t, part + parts);
+    const int rc = launch_status();
+    if (rc != MTGR_OK) return rc;
+    parts += grid;
+  }
+  // the last table first, for what L2 holds; the norm is written once
+  const int32_t last = n > 0 ? (n - 1) / N * N : 0;
+  for (int32_t i = last; i >= 0; i -= N) {
+    if (n > N) fill(t, g, i, n < i + N ? n : i + N);
+    const int grid = scale ? grid_of(t.chunk0[t.count]) : 1;
+    // (an early launch of this kernel beside the first one measured 250 against 213
+    // us on 101 M fp32 values)
+    grad_scale_kernel<N><<<grid, 256, 0, s>>>(t, part, parts, max_norm, inv_scale, scale ? 1 : 0,
+                                          i == last ? norm : nullptr, status);
+    const int rc = launch_status();
+    if (rc != MTGR_OK) return rc;
+    if (!scale) break;
+  }
+  return MTGR_OK;
 }
 
 }  // namespace
@@ -231,35 +273,8 @@ int grad_clip_launches(const mtgr_grad_tensor* g, int32_t n) {
 
 int launch_grad_clip(const mtgr_grad_tensor* g, int32_t n, float max_norm, float inv_scale, float* norm,
                      void* ws, int32_t* status, cudaStream_t s) {
-  double* part = static_cast<double*>(ws);
-  Table t;
-  t.count = 0;
-  t.chunk0[0] = 0;
-  int32_t parts = 0;
-  bool scale = false;
-  for (int32_t i = 0; i < n; i += kTable) {
-    fill(t, g, i, n < i + kTable ? n : i + kTable);
-    for (int k = 0; k < t.count; ++k) scale = scale || t.out[k] != nullptr;
-    const int grid = grid_of(t.chunk0[t.count]);
-    grad_sum_kernel<<<grid, 256, 0, s>>>(t, part + parts);
-    const int rc = launch_status();
-    if (rc != MTGR_OK) return rc;
-    parts += grid;
-  }
-  // the last table first, for what L2 holds; the norm is written once
-  const int32_t last = n > 0 ? (n - 1) / kTable * kTable : 0;
-  for (int32_t i = last; i >= 0; i -= kTable) {
-    if (n > kTable) fill(t, g, i, n < i + kTable ? n : i + kTable);
-    const int grid = scale ? grid_of(t.chunk0[t.count]) : 1;
-    // (an early launch of this kernel beside the first one measured 250 against 213
-    // us on 101 M fp32 values)
-    grad_scale_kernel<<<grid, 256, 0, s>>>(t, part, parts, max_norm, inv_scale, scale ? 1 : 0,
-                                          i == last ? norm : nullptr, status);
-    const int rc = launch_status();
-    if (rc != MTGR_OK) return rc;
-    if (!scale) break;
-  }
-  return MTGR_OK;
+  return n <= kSmallTable ? launch_n<kSmallTable>(g, n, max_norm, inv_scale, norm, ws, status, s)
+                          : launch_n<kTable>(g, n, max_norm, inv_scale, norm, ws, status, s);
 }
 
 }  // namespace mtgr
