@@ -181,7 +181,7 @@ _SIGNATURES = {
     "mtgr_quantize_rows": (ctypes.c_int, [c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_vp]),
     "mtgr_gemm_i8": (ctypes.c_int, [c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp,
                                     c_i32, c_i32, c_vp, c_vp, c_vp]),
-    "mtgr_linear_i8_workspace_bytes": (c_size, [c_i32, c_i32]),
+    "mtgr_linear_i8_workspace_bytes": (c_size, [c_i32, c_i32, c_i32]),
     "mtgr_linear_i8": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i32, c_vp, c_i64, c_vp, c_vp, c_vp,
                                       c_i32, c_vp, c_i32, c_i32, c_vp, c_vp, c_size, c_vp, c_vp]),
     "mtgr_grad_clip_workspace_bytes": (c_size, [c_vp, c_i32]),
@@ -518,8 +518,8 @@ def mtgr_gemm_i8(d_a, d_a_scale, d_b, d_b_scale, d_bias, epi, d_resid, q_cols, d
         _stream(stream)))
 
 
-def mtgr_linear_i8_workspace_bytes(M: int, K: int) -> int:
-    return load().mtgr_linear_i8_workspace_bytes(M, K)
+def mtgr_linear_i8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return load().mtgr_linear_i8_workspace_bytes(M, N, K)
 
 
 def mtgr_linear_i8(d_x, d_w, d_w_scale, d_bias, epi, d_resid, q_cols, d_out, d_ws, d_status,

@@ -575,7 +575,7 @@ MTGR_API const char* mtgr_status_string(int status) {
   }
 }
 
-MTGR_API int mtgr_version(void) { return 101; }
+MTGR_API int mtgr_version(void) { return 102; }
 
 MTGR_API int mtgr_pack_offsets(int32_t B, const int32_t* d_lens, int32_t T, int32_t* d_seg_off,
                                int32_t* d_user_off, int8_t* d_group_id, int32_t* d_status,

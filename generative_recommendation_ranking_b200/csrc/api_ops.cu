@@ -15,6 +15,7 @@ namespace {
 constexpr int32_t kMaxRowD = 8192;         // as for mtgr_group_layernorm
 constexpr int32_t kMaxQuantK = 32768;      // a row stays in one block's registers
 constexpr int32_t kMaxI8K = 131072;        // exclusive: 2^14 K < 2^31 for any bytes
+constexpr int32_t kMaxI8Rows = 1 << 30;    // row and column indices of whole tiles stay in 32 bits
 constexpr int64_t kMaxGradElems = 1ll << 38;
 
 inline cudaStream_t as_stream(mtgr_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -49,7 +50,7 @@ int gemm_i8_check(int32_t M, int32_t N, int32_t K, const void* b, const float* s
   if (epi != MTGR_EPI_NONE && epi != MTGR_EPI_SILU && epi != MTGR_EPI_RESID) return MTGR_ERR_INVALID_ARG;
   if (epi == MTGR_EPI_RESID && out_dtype != MTGR_F32) return MTGR_ERR_INVALID_ARG;
   if (out_dtype != MTGR_F32 && out_dtype != MTGR_BF16 && out_dtype != MTGR_F16) return MTGR_ERR_UNSUPPORTED;
-  if (K % 16 != 0 || N % 8 != 0 || K >= kMaxI8K) return MTGR_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || N % 8 != 0 || K >= kMaxI8K || M > kMaxI8Rows || N > kMaxI8Rows) return MTGR_ERR_UNSUPPORTED;
   if (M > 0 && N > 0 &&
       (b == nullptr || sb == nullptr || out == nullptr || (epi == MTGR_EPI_RESID && resid == nullptr)))
     return MTGR_ERR_INVALID_ARG;
@@ -68,6 +69,7 @@ int quant_check(int32_t M, int32_t K, int32_t x_dtype, const void* x, int64_t ld
 
 int grads_check(const mtgr_grad_tensor* g, int32_t n) {
   if (n < 0 || (n > 0 && g == nullptr)) return MTGR_ERR_INVALID_ARG;
+  int32_t first = -1;  // the first tensor that is not empty
   for (int32_t i = 0; i < n; ++i) {
     if (g[i].n < 0 || g[i].n > kMaxGradElems || (g[i].n > 0 && g[i].g == nullptr)) return MTGR_ERR_INVALID_ARG;
     const int e = dtype_size(g[i].dtype), eo = dtype_size(g[i].out_dtype);
@@ -77,7 +79,9 @@ int grads_check(const mtgr_grad_tensor* g, int32_t n) {
       return MTGR_ERR_INVALID_ARG;
     // in place only in the same type; outputs for all tensors or for none
     if (g[i].out == g[i].g && g[i].out != nullptr && g[i].out_dtype != g[i].dtype) return MTGR_ERR_INVALID_ARG;
-    if (g[i].n > 0 && g[0].n > 0 && (g[i].out == nullptr) != (g[0].out == nullptr)) return MTGR_ERR_INVALID_ARG;
+    if (g[i].n == 0) continue;
+    if (first < 0) first = i;
+    if ((g[i].out == nullptr) != (g[first].out == nullptr)) return MTGR_ERR_INVALID_ARG;
   }
   return MTGR_OK;
 }
@@ -168,15 +172,15 @@ MTGR_API int mtgr_gemm_i8(int32_t M, int32_t N, int32_t K, const int8_t* d_a, co
   if ((M > 0 && N > 0 && (d_a == nullptr || d_a_scale == nullptr)) || !aligned16(d_a)) return MTGR_ERR_INVALID_ARG;
   if (!device_is_sm100()) return MTGR_ERR_UNSUPPORTED;
   TimedScope tsc(MTGR_TIMER_GEMM_QKVU, as_stream(stream), M > 0 && N > 0 ? 1 : 0);
-  if (gemm_i8_is_few(M, K))
+  if (gemm_i8_is_few(M, N, K))
     return launch_gemm_i8_few(M, N, K, MTGR_I8, d_a, K, d_a_scale, d_b, d_b_scale, d_bias, epi, d_resid, q_cols,
                               out_dtype, d_out, d_status, as_stream(stream));
   return launch_gemm_i8(M, N, K, d_a, d_a_scale, d_b, d_b_scale, d_bias, epi, d_resid, q_cols, out_dtype, d_out,
                         d_status, as_stream(stream));
 }
 
-MTGR_API size_t mtgr_linear_i8_workspace_bytes(int32_t M, int32_t K) {
-  if (M < 0 || K <= 0 || gemm_i8_is_few(M, K)) return 0;
+MTGR_API size_t mtgr_linear_i8_workspace_bytes(int32_t M, int32_t N, int32_t K) {
+  if (M < 0 || N < 0 || K <= 0 || gemm_i8_is_few(M, N, K)) return 0;
   return align_up((size_t)M * (size_t)K, 256) + align_up((size_t)M * 4, 256);
 }
 
@@ -188,7 +192,7 @@ MTGR_API int mtgr_linear_i8(int32_t M, int32_t N, int32_t K, int32_t x_dtype, co
   if (rc != MTGR_OK) return rc;
   rc = quant_check(M, K, x_dtype, d_x, ld_x);
   if (rc != MTGR_OK) return rc;
-  const size_t need = mtgr_linear_i8_workspace_bytes(M, K);
+  const size_t need = mtgr_linear_i8_workspace_bytes(M, N, K);
   if (ws_bytes < need) return MTGR_ERR_CAPACITY;
   if ((need > 0 && d_ws == nullptr) || !aligned16(d_ws)) return MTGR_ERR_INVALID_ARG;
   if (!device_is_sm100()) return MTGR_ERR_UNSUPPORTED;

@@ -1,7 +1,7 @@
 // The int8 product for few rows (a chunk of candidates, a single token), in one
 // kernel from float rows to the output: latency counts here, not bandwidth.
 //
-//   out[m][n] = epi(sa[m] sb[n] sum_k a[m][k] b[n][k] + bias[n]),  m < 16 MT
+//   out[m][n] = epi(sa[m] sb[n] sum_k a[m][k] b[n][k] + bias[n]),  M <= 16
 //
 // A block takes 16 output channels. Its warps first ask for their share of the
 // weights (each warp an eighth of k: 16 bytes a lane and load), then quantise the
@@ -10,8 +10,10 @@
 // mma.sync m16n8k32 on signed bytes. The k order within an instruction does not
 // matter as long as a and b share it, so a lane's 16 consecutive bytes serve two
 // instructions. The warps' exact int32 sums meet in shared memory.
-// Against quantiser + 128 x 64 tcgen05 tiles at 8 x 2048 x 512: 10.2 us of kernels in
-// two launches there, one launch here.
+// In a graph, bf16 rows, against the quantiser and 128 x 64 tcgen05 tiles: 8 x 2048 x
+// 512 3.5 us (5.4 there), 8 x 1024 x 4096 8.7 (14.2), 16 x 4096 x 1024 5.4 (7.2). With
+// more rows, or with more blocks than two an SM, quantising in every block costs
+// more than it saves: 32 x 2048 x 512 took 6.4 (5.4), 16 x 8192 x 512 7.7 (6.2).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -26,6 +28,7 @@ namespace mtgr {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kRows = 16;      // rows of an instruction
 constexpr int kCols = 16;      // output channels a block
 constexpr int kAheadK = 4;     // 64-byte k groups a warp has in flight per channel tile
 
@@ -86,10 +89,10 @@ __device__ __forceinline__ float take_row(const FewArgs& a, int r, uint8_t* to, 
   return s;
 }
 
-template <typename TX, int MT>
+template <typename TX>
 __global__ void __launch_bounds__(32 * kWarps) gemm_i8_few_kernel(FewArgs a, int epi, int out_dtype) {
-  extern __shared__ __align__(16) uint8_t rows[];  // [16 MT][stride], then the warps' sums
-  __shared__ float row_s[16 * MT];
+  extern __shared__ __align__(16) uint8_t rows[];  // [16][stride], then the warps' sums
+  __shared__ float row_s[kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, q = lane & 3;  // the lane's row (channel) and its 16 bytes of a k group
   const int groups = (a.K + 63) >> 6;
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(32 * kWarps) gemm_i8_few_kernel(FewArgs a, int
   };
 #pragma unroll
   for (int i = 0; i < kAheadK; ++i) fetch(g0 + i, w, i);
-  for (int r = warp; r < 16 * MT; r += kWarps) {
+  for (int r = warp; r < kRows; r += kWarps) {
     if (r < a.M) {
       const float s = take_row<TX>(a, r, rows + r * stride, lane);
       if (lane == 0) row_s[r] = s;
@@ -119,26 +122,17 @@ __global__ void __launch_bounds__(32 * kWarps) gemm_i8_few_kernel(FewArgs a, int
     }
   }
   __syncthreads();
-  int c[MT][2][4];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[m][t][i] = 0;
+  int c[2][4] = {};
   for (int kg = g0; kg < g1; kg += kAheadK) {
 #pragma unroll
     for (int i = 0; i < kAheadK; ++i) {
       if (kg + i < g1) {
+        const uint8_t* p = rows + g * stride + 64 * (kg + i) + 16 * q;
+        const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8 * stride);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint8_t* p = rows + (16 * m + g) * stride + 64 * (kg + i) + 16 * q;
-          const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8 * stride);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            mma_s8(c[m][t], x.x, y.x, x.y, y.y, w[t][i].x, w[t][i].y);
-            mma_s8(c[m][t], x.z, y.z, x.w, y.w, w[t][i].z, w[t][i].w);
-          }
+        for (int t = 0; t < 2; ++t) {
+          mma_s8(c[t], x.x, y.x, x.y, y.y, w[t][i].x, w[t][i].y);
+          mma_s8(c[t], x.z, y.z, x.w, y.w, w[t][i].z, w[t][i].w);
         }
       }
       fetch(kg + kAheadK + i, w, i);
@@ -148,22 +142,20 @@ __global__ void __launch_bounds__(32 * kWarps) gemm_i8_few_kernel(FewArgs a, int
   __syncthreads();  // the rows are done with: their memory takes the sums
   int* part = reinterpret_cast<int*>(rows);
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      int* p = part + (warp * 16 * MT + 16 * m + g) * kCols + 8 * t + 2 * q;
-      p[0] = c[m][t][0];
-      p[1] = c[m][t][1];
-      p[8 * kCols] = c[m][t][2];
-      p[8 * kCols + 1] = c[m][t][3];
-    }
+  for (int t = 0; t < 2; ++t) {
+    int* p = part + (warp * kRows + g) * kCols + 8 * t + 2 * q;
+    p[0] = c[t][0];
+    p[1] = c[t][1];
+    p[8 * kCols] = c[t][2];
+    p[8 * kCols + 1] = c[t][3];
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * MT * kCols; i += 32 * kWarps) {
+  for (int i = threadIdx.x; i < kRows * kCols; i += 32 * kWarps) {
     const int m = i / kCols, n = n0 + i % kCols;
     if (m >= a.M || n >= a.N) continue;
     int s = 0;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) s += part[k * 16 * MT * kCols + i];
+    for (int k = 0; k < kWarps; ++k) s += part[k * kRows * kCols + i];
     float v = __int2float_rn(s) * (row_s[m] * a.sb[n]);
     if (a.bias != nullptr) v += a.bias[n];
     if (epi == MTGR_EPI_SILU) v = __fdividef(v, 1.0f + __expf(-v));
@@ -185,18 +177,15 @@ __global__ void __launch_bounds__(32 * kWarps) gemm_i8_few_kernel(FewArgs a, int
 
 constexpr int kMaxRowsBytes = 100 * 1024;
 
-int m_tiles(int M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
-
-int smem_bytes(int M, int K) {
-  const int mt = m_tiles(M);
-  const int rows = 16 * mt * (((K + 63) / 64) * 64 + 64), sums = kWarps * 16 * mt * kCols * 4;
+int smem_bytes(int K) {
+  const int rows = kRows * (((K + 63) / 64) * 64 + 64), sums = kWarps * kRows * kCols * 4;
   return rows > sums ? rows : sums;
 }
 
-template <typename TX, int MT>
+template <typename TX>
 int launch_t(const FewArgs& a, int epi, int32_t out_dtype, cudaStream_t s) {
-  const int bytes = smem_bytes(a.M, a.K);
-  auto kern = gemm_i8_few_kernel<TX, MT>;
+  const int bytes = smem_bytes(a.K);
+  auto kern = gemm_i8_few_kernel<TX>;
   if (bytes > 40 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return MTGR_ERR_CUDA;
@@ -204,19 +193,13 @@ int launch_t(const FewArgs& a, int epi, int32_t out_dtype, cudaStream_t s) {
   return launch_status();
 }
 
-template <typename TX>
-int launch_m(const FewArgs& a, int epi, int32_t out_dtype, cudaStream_t s) {
-  switch (m_tiles(a.M)) {
-    case 1: return launch_t<TX, 1>(a, epi, out_dtype, s);
-    case 2: return launch_t<TX, 2>(a, epi, out_dtype, s);
-    default: return launch_t<TX, 4>(a, epi, out_dtype, s);
-  }
-}
-
 }  // namespace
 
-// Few rows: at most 64, whose bytes fit a block's shared memory.
-bool gemm_i8_is_few(int32_t M, int32_t K) { return M <= 64 && smem_bytes(M, K) <= kMaxRowsBytes; }
+// Few rows and channels: one instruction's rows, at most two blocks an SM, and a
+// block's bytes of the rows fit its shared memory.
+bool gemm_i8_is_few(int32_t M, int32_t N, int32_t K) {
+  return M <= kRows && N <= kCols * 2 * device_sm_count() && K <= 8192 && smem_bytes(K) <= kMaxRowsBytes;
+}
 
 // x_dtype MTGR_I8: x are bytes with scales sa; else float rows, quantised here.
 int launch_gemm_i8_few(int M, int N, int K, int32_t x_dtype, const void* x, int64_t ld_x, const float* sa,
@@ -225,10 +208,10 @@ int launch_gemm_i8_few(int M, int N, int K, int32_t x_dtype, const void* x, int6
   if (M == 0 || N == 0) return MTGR_OK;
   const FewArgs a{M, N, K, x, ld_x, sa, b, sb, bias, resid, out, q_cols, status};
   switch (x_dtype) {
-    case MTGR_I8: return launch_m<int8_t>(a, epi, out_dtype, s);
-    case MTGR_F32: return launch_m<float>(a, epi, out_dtype, s);
-    case MTGR_BF16: return launch_m<__nv_bfloat16>(a, epi, out_dtype, s);
-    case MTGR_F16: return launch_m<__half>(a, epi, out_dtype, s);
+    case MTGR_I8: return launch_t<int8_t>(a, epi, out_dtype, s);
+    case MTGR_F32: return launch_t<float>(a, epi, out_dtype, s);
+    case MTGR_BF16: return launch_t<__nv_bfloat16>(a, epi, out_dtype, s);
+    case MTGR_F16: return launch_t<__half>(a, epi, out_dtype, s);
     default: return MTGR_ERR_UNSUPPORTED;
   }
 }

@@ -168,11 +168,12 @@ __global__ void __launch_bounds__(256) grad_scale_kernel(const __grid_constant__
   for (int i = threadIdx.x; i < parts; i += blockDim.x) s += part[i];
   s = block_sum(s);
   const double norm = sqrt(s) * (double)inv_scale;
+  const bool finite = isfinite((float)norm);
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out != nullptr) {
     *norm_out = (float)norm;
-    if (!isfinite(norm)) set_status(status, MTGR_ERR_RANGE);
+    if (!finite) set_status(status, MTGR_ERR_RANGE);
   }
-  if (scale == 0 || !isfinite(norm)) return;
+  if (scale == 0 || !finite) return;
   const float ratio = (float)((double)max_norm / (norm + 1e-6));
   const float c = inv_scale * fminf(1.0f, ratio);
   const int chunks = t.chunk0[t.count];
@@ -227,7 +228,7 @@ int launch_n(const mtgr_grad_tensor* g, int32_t n, float max_norm, float inv_sca
   bool scale = false;
   for (int32_t i = 0; i < n; i += N) {
     fill(t, g, i, n < i + N ? n : i + N);
-    for (int k = 0; k < t.count; ++k) scale = scale || t.out[k] != nullptr;
+    for (int k = 0; k < t.count; ++k) scale = scale || (t.n[k] > 0 && t.out[k] != nullptr);
     const int grid = grid_of(t.chunk0[t.count]);
     grad_sum_kernel<N><<<grid, 256, 0, s>>>(t, part + parts);
     const int rc = launch_status();
@@ -267,7 +268,7 @@ size_t grad_clip_ws_bytes(const mtgr_grad_tensor* g, int32_t n) {
 int grad_clip_launches(const mtgr_grad_tensor* g, int32_t n) {
   const int tables = (n + kTable - 1) / kTable;
   for (int32_t i = 0; i < n; ++i)
-    if (g[i].out != nullptr) return 2 * tables;
+    if (g[i].n > 0 && g[i].out != nullptr) return 2 * tables;
   return tables + 1;
 }
 

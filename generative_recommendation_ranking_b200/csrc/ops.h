@@ -77,7 +77,7 @@ int launch_gemm_i8(int M, int N, int K, const int8_t* a, const float* sa, const 
                    int32_t out_dtype, void* out, int32_t* status, cudaStream_t s, bool dependent = false);
 
 // the same in one kernel from float rows or bytes (MTGR_I8, with sa), for few rows
-bool gemm_i8_is_few(int32_t M, int32_t K);
+bool gemm_i8_is_few(int32_t M, int32_t N, int32_t K);
 int launch_gemm_i8_few(int M, int N, int K, int32_t x_dtype, const void* x, int64_t ld_x, const float* sa,
                        const int8_t* b, const float* sb, const float* bias, int epi, const float* resid, int q_cols,
                        int32_t out_dtype, void* out, int32_t* status, cudaStream_t s);

@@ -303,7 +303,7 @@ def linear_i8(x, w, w_scale, x_scale=None, bias=None, epi: int = MTGR_EPI_NONE, 
     if x_scale is not None:
         raise ValueError("x_scale goes with int8 rows")
     ld = _given_rows("x", x, (M, K), _FLOATS, dev)
-    need = _lib.load().mtgr_linear_i8_workspace_bytes(M, K)
+    need = _lib.load().mtgr_linear_i8_workspace_bytes(M, N, K)
     if need == 0:
         p, room = None, 0
     elif ws is None or ws.numel() * ws.element_size() < need:
@@ -411,6 +411,7 @@ def _clip(ws, grads, table, max_norm, inv_scale, norm, status, stream):
         _given("status", status, (1,), torch.int32, dev)
     if other is not None:
         ws.record_stream(other)
+        grads.status.record_stream(other)
     _lib.check("mtgr_grad_clip", _lib.load().mtgr_grad_clip(
         table, len(table), max_norm, inv_scale, norm.data_ptr(), ws.data_ptr(), ws.numel(), status.data_ptr(), raw))
     return norm

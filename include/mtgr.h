@@ -751,7 +751,7 @@ MTGR_API int mtgr_quantize_rows(int32_t M, int32_t K, int32_t x_dtype, const voi
  * internal wait that ran out leaves MTGR_ERR_TIMEOUT; with d_status NULL both go
  * unseen. q_cols > 0 (a multiple of 32) halves columns [0, q_cols) at the end.
  *   d_a [M][K], d_b [N][K] int8; d_out, d_resid [M][N], distinct buffers
- *   K % 16 == 0, K < 131072, N % 8 == 0; d_a, d_b, d_b_scale, d_bias, d_resid,
+ *   K % 16 == 0, K < 131072, N % 8 == 0, M and N at most 2^30; d_a, d_b, d_b_scale, d_bias, d_resid,
  *   d_out 16-byte aligned
  * Runs on tcgen05. Timer class MTGR_TIMER_GEMM_QKVU, as mtgr_gemm.
  */
@@ -766,7 +766,7 @@ MTGR_API int mtgr_gemm_i8(int32_t M, int32_t N, int32_t K, const int8_t* d_a, co
  * quantised within the product's kernel, and d_ws may then be NULL) and multiplies
  * as mtgr_gemm_i8; the arguments and limits are theirs.
  */
-MTGR_API size_t mtgr_linear_i8_workspace_bytes(int32_t M, int32_t K);
+MTGR_API size_t mtgr_linear_i8_workspace_bytes(int32_t M, int32_t N, int32_t K);
 MTGR_API int mtgr_linear_i8(int32_t M, int32_t N, int32_t K, int32_t x_dtype, const void* d_x,
                             int64_t ld_x, const int8_t* d_w, const float* d_w_scale,
                             const float* d_bias, int32_t epi, const float* d_resid, int32_t q_cols,

@@ -124,16 +124,19 @@ def test_int8_product_refusals(lib):
                     dict(epi=_lib.MTGR_EPI_RESID, od=F32), dict(epi=_lib.MTGR_EPI_RESID, resid=F),
                     dict(epi=_lib.MTGR_EPI_RESID, resid=F + 4, od=F32)):
             assert f(**bad) == INVALID, (f.__name__, bad)
+        assert f(M=(1 << 30) + 1) == UNSUPPORTED and f(N=(1 << 30) + 8) == UNSUPPORTED
         assert f(N=60) == UNSUPPORTED and f(od=I8) == UNSUPPORTED
     assert gemm(K=72) == UNSUPPORTED and linear(K=72, ld=72) == UNSUPPORTED
     assert gemm(K=131072) == UNSUPPORTED and linear(K=32784, ld=32784) == UNSUPPORTED
     assert gemm(a=None) == INVALID and gemm(sa=None) == INVALID and gemm(a=F + 4) == INVALID
     assert linear(x=None) == INVALID and linear(ld=8) == INVALID and linear(xd=I8) == UNSUPPORTED
     assert linear(ws=None) == INVALID and linear(ws_bytes=100) == CAPACITY
-    assert _lib.mtgr_linear_i8_workspace_bytes(100, 48) == 4864 + 512
-    assert _lib.mtgr_linear_i8_workspace_bytes(64, 512) == 0 and _lib.mtgr_linear_i8_workspace_bytes(64, 4096) > 0
-    assert _lib.mtgr_linear_i8_workspace_bytes(-1, 48) == 0 and _lib.mtgr_linear_i8_workspace_bytes(5, 0) == 0
-    assert _lib.mtgr_linear_i8_workspace_bytes(1 << 20, 8192) == (1 << 33) + (1 << 22)
+    size = _lib.mtgr_linear_i8_workspace_bytes
+    assert size(100, 64, 48) == 4864 + 512 and size(100, 64, 4096) == 409600 + 512
+    # few rows and columns are quantised within the product
+    assert size(16, 16, 512) == 0 and size(17, 16, 512) > 0 and size(16, 1 << 20, 512) > 0 and size(16, 16, 32768) > 0
+    assert size(-1, 8, 48) == 0 and size(5, -8, 48) == 0 and size(5, 8, 0) == 0
+    assert size(1 << 20, 64, 8192) == (1 << 33) + (1 << 22)
 
 
 def test_grad_clip_refusals(lib):
@@ -150,6 +153,8 @@ def test_grad_clip_refusals(lib):
         assert clip(t) == INVALID, (t.g, t.n)
     assert clip(G(F, F, 100, I8, I8)) == UNSUPPORTED and clip(G(F, F, 100, F32, BF16)) == UNSUPPORTED
     assert clip(ok, G(F, None, 5, F32, F32)) == INVALID  # outputs for all tensors or none
+    assert clip(G(None, None, 0, F32, F32), ok, G(F, None, 5, F32, F32)) == INVALID  # empty ones aside
+    assert clip(G(None, F, 0, F32, F32), G(F, None, 5, F32, F32), G(F, F, 5, F32, F32)) == INVALID
     for bad in (dict(max_norm=-1.0), dict(max_norm=float("nan")), dict(inv=0.0), dict(inv=float("inf")),
                 dict(inv=float("nan")), dict(norm=None), dict(status=None), dict(ws=None)):
         assert clip(ok, **bad) == INVALID, bad
