@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
   bool range_bad = false;
 
   auto flush = [&]() {
-    if (g_run < 0) return;
+    if (g_run < 0 || rows <= 0) return;  // a team past the last one has no slots
     float* p = slots + (int64_t)g_run * kSlots * d;
     const bool add = (seen >> g_run) & 1u;
 #pragma unroll

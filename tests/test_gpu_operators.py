@@ -193,6 +193,33 @@ def test_boundary_in_place_and_rows_left_alone():
     assert torch.equal(dev["x"][n:], keep[n:]) and (y[n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("T,d", [(1, 8), (5, 64), (3, 104), (7, 256), (5, 512), (3, 1000), (2, 2048)])
+def test_boundary_writes_its_rows_alone(T, d):
+    dev, _ = case(T, d)
+    h = torch.full((T + 40, d), 7.0, device="cuda")
+    y = torch.full((T + 40, d), 77, dtype=torch.int8, device="cuda")
+    ys = torch.full((T + 40,), 9.0, device="cuda")
+    mt.boundary_forward(**dev, h=h[16:16 + T], y=y[16:16 + T], y_scale=ys[16:16 + T], y_dtype=torch.int8)
+    for t, v in ((h, 7), (y, 77), (ys, 9)):
+        assert (t[:16] == v).all() and (t[16 + T:] == v).all()
+    # gradients into wide rows: what lies past d stays
+    L = mt._lib
+    do, du = (torch.full((T + 8, d + 24), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dx = torch.full((T + 8, d), 3.0, device="cuda")
+    dh, dy = upstream(T, d)
+    want = mt.boundary_backward(**dev, dh=dh, dy=dy)
+    par = {n: torch.empty(4, d, device="cuda") for n in NAMES}
+    p = L.MtgrBoundaryParams(d, 4, EPS, L.MTGR_GATE_LINEAR, *[dev[n].data_ptr() for n in NAMES])
+    gr = L.MtgrBoundaryGrads(*[par[n].data_ptr() for n in NAMES])
+    ws = torch.empty(max(256, L.mtgr_boundary_bwd_workspace_bytes(T, p)), dtype=torch.uint8, device="cuda")
+    L.mtgr_boundary_bwd(p, T, dev["group_id"], dev["o"], dev["u"], dev["x"], dh, dy, do[4:4 + T], du[4:4 + T], dx[4:4 + T], gr, ws)
+    assert torch.equal(do[4:4 + T, :d], want["do"]) and torch.equal(du[4:4 + T, :d], want["du"]) and torch.equal(dx[4:4 + T], want["dx"])
+    assert all(torch.equal(par[n], want[n]) for n in NAMES)
+    for t in (do, du, dx):
+        assert (t[:4] == 3).all() and (t[4 + T:] == 3).all()
+    assert (do[:, d:] == 3).all() and (du[:, d:] == 3).all()
+
+
 def test_boundary_no_rows():
     dev, _ = case(0, 64)
     h, y, ys = mt.boundary_forward(**dev, y_dtype=torch.int8)
@@ -285,6 +312,21 @@ def test_boundary_backward_same_bits_every_time():
     assert all(torch.equal(a[k], b[k]) for k in a)
 
 
+@pytest.mark.parametrize("d", [8, 64, 104, 128, 256, 264, 512, 1024])
+@pytest.mark.parametrize("T", [1, 21, 77, 20011])
+def test_boundary_backward_keeps_to_its_workspace(d, T):
+    # the workspace exactly as large as asked for, in the middle of a larger buffer;
+    # teams that do not fill a block write nothing
+    dev, r = case(T, d)
+    dh, dy = upstream(T, d)
+    p = mt._lib.MtgrBoundaryParams(d, 4, EPS, mt.MTGR_GATE_LINEAR, 16, 16, 16, 16, 16)
+    need = mt.mtgr_boundary_bwd_workspace_bytes(T, p)
+    pad = 1 << 20
+    buf = torch.full((pad + need + pad,), 0xA5, dtype=torch.uint8, device="cuda")
+    mt.boundary_backward(**dev, dh=dh, dy=dy, ws=buf[pad:pad + need])
+    assert (buf[:pad] == 0xA5).all() and (buf[pad + need:] == 0xA5).all()
+
+
 def test_boundary_backward_f16_range_is_reported():
     dev, _ = case(8, 512, torch.float16)
     dh, dy = upstream(8, 512)
@@ -345,6 +387,14 @@ def test_quantize_borders_and_special_rows():
     wq, ws = op.quantize_rows(x)
     assert np.array_equal(s.cpu().numpy(), ws, equal_nan=True) and np.array_equal(q.cpu().numpy(), wq)
     assert np.isnan(ws[-3:]).all()
+
+
+@pytest.mark.parametrize("M,K", [(3, 8), (5, 520), (7, 2056), (9, 4104)])
+def test_quantize_writes_its_rows_alone(M, K):
+    q = torch.full((M + 16, K), 99, dtype=torch.int8, device="cuda")
+    s = torch.full((M + 16,), 3.0, device="cuda")
+    mt.quantize_rows(torch.randn(M, K, device="cuda"), q[8:8 + M], s[8:8 + M])
+    assert (q[:8] == 99).all() and (q[8 + M:] == 99).all() and (s[:8] == 3).all() and (s[8 + M:] == 3).all()
 
 
 def test_quantize_strided_rows():
@@ -437,6 +487,17 @@ def test_linear_is_quantise_then_product(M, dtype):
         assert torch.equal(mt.linear_i8(x, w, ws, bias=bias, epi=epi), mt.gemm_i8(q, s, w, ws, bias, epi))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (16, 72, 528), (17, 200, 64), (129, 520, 144), (9000, 1160, 512), (9001, 1000, 640)])
+@pytest.mark.parametrize("out", [torch.float32, torch.float16])
+def test_product_writes_its_rows_alone(M, N, K, out):
+    a, sa, b, sb, _, _ = product_case(M, N, K)
+    g = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    buf = torch.full((M + 300, N), 7.0, dtype=out, device="cuda")
+    mt.gemm_i8(g(a), g(sa), g(b), g(sb), out_dtype=out, out=buf[8:8 + M])
+    assert (buf[:8] == 7).all() and (buf[8 + M:] == 7).all()
+    assert torch.equal(buf[8:8 + M], mt.gemm_i8(g(a), g(sa), g(b), g(sb), out_dtype=out))
+
+
 def test_product_no_rows_or_columns():
     w, ws = torch.zeros(64, 128, dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
     assert mt.linear_i8(torch.zeros(0, 128, device="cuda"), w, ws).shape == (0, 64)
@@ -492,6 +553,22 @@ def test_clip_odd_addresses():
     outs = [torch.empty(x.numel() + 3, dtype=x.dtype, device="cuda")[i % 3:][:x.numel()] for i, x in enumerate(grads)]
     check_clip(grads, outs, 0.1, 1.0)
     check_clip(grads, None, 0.1, 1.0)
+
+
+@pytest.mark.parametrize("shift", [0, 1, 3, 4])
+@pytest.mark.parametrize("dtype,to", [(torch.float32, torch.float32), (torch.bfloat16, torch.float32), (torch.float16, torch.float16)])
+def test_clip_writes_its_tensors_alone(dtype, to, shift):
+    sizes = [1, 7, 8, 100, 16384, 16391, 40000]
+    grads, outs, buf = [], [], torch.full((sum(sizes) + 64 * len(sizes),), 5.0, dtype=to, device="cuda")
+    at = 16 + shift
+    inside = torch.zeros(buf.numel(), dtype=torch.bool, device="cuda")
+    for i, n in enumerate(sizes):
+        grads.append(torch.randn(n + 8, device="cuda").to(dtype)[i % 5:][:n])
+        outs.append(buf[at:at + n])
+        inside[at:at + n] = True
+        at += n + 40 + i
+    check_clip(grads, outs, 0.1, 1.0)
+    assert (buf[~inside] == 5).all()
 
 
 @pytest.mark.parametrize("scale", [1e-30, 1e-22, 1e19, 1e30])
