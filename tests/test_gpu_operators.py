@@ -648,6 +648,31 @@ def test_on_another_stream_and_in_a_graph():
         assert all(torch.equal(p, q) for p, q in zip(want, got)), k
 
 
+def test_two_streams_at_once():
+    # calls that overlap on the GPU keep apart: workspaces are each call's own
+    devs = [case(3000, 512, seed=i)[0] for i in range(2)]
+    ups = [upstream(3000, 512, seed=i) for i in range(2)]
+    w, ws = mt.quantize_rows(torch.randn(1024, 512, device="cuda"))
+
+    def work(i, stream):
+        out = []
+        for _ in range(8):
+            h, y, ys = mt.boundary_forward(**devs[i], y_dtype=torch.int8, stream=stream)
+            out += [h, y, ys, mt.gemm_i8(y, ys, w, ws, stream=stream), mt.linear_i8(h, w, ws, stream=stream),
+                    mt.linear_i8(h[:7], w, ws, stream=stream)]
+            b = mt.boundary_backward(**devs[i], dh=ups[i][0], dy=ups[i][1], stream=stream)
+            out += list(b.values())
+        return out
+
+    want = [work(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [work(i, streams[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_serving_block_from_boundary_to_mlp():
     """One block's products in int8, from the boundary before it to its second MLP
     product, against the same steps in float64 on the same quantised weights:
