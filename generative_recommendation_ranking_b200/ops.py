@@ -373,8 +373,10 @@ class GradientSet:
         with torch.cuda.device(self.device):
             # one for each of the two calls, so that a norm may run beside a clip
             size = _lib.mtgr_grad_clip_workspace_bytes(self.c, n)
-            self.ws, self.ws_norm = (torch.empty(size, dtype=torch.uint8, device=self.device) for _ in range(2))
+            self.ws, self.ws_norm = (torch.zeros(size, dtype=torch.uint8, device=self.device) for _ in range(2))
             self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()  # zeros before a clip on any stream
 
     def clip(self, max_norm: float, inv_scale: float = 1.0, norm=None, status=None, stream=None) -> torch.Tensor:
         """Clips to ``max_norm`` after taking the loss scale out (``inv_scale`` = 1 /
@@ -389,7 +391,8 @@ class GradientSet:
 
     def check(self) -> None:
         """Synchronise and raise if a call on this set met a norm that is not
-        finite; the word is then cleared for the next step."""
+        finite, or ran into the limit of its waits; the word is then cleared
+        for the next step."""
         torch.cuda.synchronize(self.device)
         st = int(self.status.item())
         if st != 0:

@@ -796,7 +796,12 @@ typedef struct mtgr_grad_tensor {
  * every run. A norm that is not finite leaves the outputs untouched and
  * MTGR_ERR_RANGE in d_status (a step to skip). max_norm >= 0 (infinity: no
  * clipping), inv_scale > 0 and finite. Workspace: mtgr_grad_clip_workspace_bytes
- * (0 on invalid arguments). Timer class MTGR_TIMER_BWD_ROWS.
+ * (0 on invalid arguments), zeroed by the caller before its first use; every call
+ * leaves it fit for the next, and calls that share it are ordered. A small set runs
+ * as one kernel whose blocks meet (a cooperative launch); should one not arrive
+ * within the limit of every internal wait, MTGR_ERR_TIMEOUT is in d_status and norm
+ * and outputs hold nothing of use.
+ * Timer class MTGR_TIMER_BWD_ROWS.
  */
 MTGR_API size_t mtgr_grad_clip_workspace_bytes(const mtgr_grad_tensor* h_grads, int32_t n);
 MTGR_API int mtgr_grad_clip(const mtgr_grad_tensor* h_grads, int32_t n, float max_norm,

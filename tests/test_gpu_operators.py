@@ -602,6 +602,61 @@ def test_clip_norm_alone_and_overlaps():
     mt.GradientSet([flat, flat], [torch.zeros(100, device="cuda"), torch.zeros(100, device="cuda")])  # read twice: fine
 
 
+def held_values():  # the most values of one tensor that the one-kernel form takes
+    return torch.cuda.get_device_properties(0).multi_processor_count * 2 * 4 * 4096
+
+
+@pytest.mark.parametrize("more", [-1, 0, 1, 5000])
+@pytest.mark.parametrize("rest", [[], [0, 3, 0]])
+def test_clip_at_the_border_of_the_forms(more, rest):
+    sizes = [held_values() + more - sum(4096 for n in rest if n)] + rest
+    for to in (torch.float32, torch.bfloat16):
+        grads = clip_case(sizes, (torch.bfloat16,))
+        outs = [torch.full((x.numel() + 64,), 5.0, dtype=to, device="cuda") for x in grads]
+        check_clip(grads, [o[32:32 + x.numel()] for o, x in zip(outs, grads)], 0.5, 0.25)
+        assert all((o[:32] == 5).all() and (o[32 + x.numel():] == 5).all() for o, x in zip(outs, grads))
+
+
+def test_clip_again_and_again():
+    # a set's workspace is left fit for the next call: many in a row, no wait between, then in a graph
+    grads = clip_case([70001, 0, 300, 500000], (torch.float32, torch.bfloat16))
+    outs = [torch.empty_like(x) for x in grads]
+    s = mt.GradientSet(grads, outs)
+    want = s.clip(0.5, 0.25)
+    first = [o.clone() for o in outs]
+    norms = [s.clip(0.5, 0.25) for _ in range(200)]
+    assert all(torch.equal(n, want) for n in norms)
+    assert (s.ws[:8] == 0).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pair = [s.clip(0.5, 0.25), s.norm(0.25)]
+    for _ in range(50):
+        for o in outs:
+            o.fill_(7.0)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(n, want) for n in pair) and all(torch.equal(a, b) for a, b in zip(outs, first))
+    s.check()
+
+
+def test_clips_of_two_sets_at_once():
+    # each a cooperative kernel over the whole GPU: neither may keep the other from ending
+    sets, streams, want = [], [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(2):
+        grads = clip_case([held_values() - 8192 * (i + 1), 77], (torch.float32,), seed=i)
+        sets.append(mt.GradientSet(grads, [torch.empty_like(x) for x in grads]))
+        want.append(sets[i].clip(0.5))
+    torch.cuda.synchronize()
+    norms = [[], []]
+    for _ in range(30):
+        for i in range(2):
+            norms[i].append(sets[i].clip(0.5, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(n, want[i]) for n in norms[i])
+        sets[i].check()
+
+
 # ------------------------------------------- streams, graphs, run together --
 def test_on_another_stream_and_in_a_graph():
     dev, _ = case(600, 512)

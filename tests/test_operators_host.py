@@ -160,7 +160,7 @@ def test_grad_clip_refusals(lib):
         assert clip(ok, **bad) == INVALID, bad
     assert clip(ok, ws_bytes=0) == CAPACITY
     assert _lib.mtgr_grad_clip_workspace_bytes((G * 1)(G(None, F, 5, F32, F32)), 1) == 0
-    assert _lib.mtgr_grad_clip_workspace_bytes((G * 1)(ok), 1) == 256
+    assert _lib.mtgr_grad_clip_workspace_bytes((G * 1)(ok), 1) >= 512
 
 
 def test_python_refuses_host_tensors():
