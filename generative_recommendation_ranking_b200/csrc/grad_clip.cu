@@ -371,9 +371,8 @@ int launch_n(const mtgr_grad_tensor* g, int32_t n, float max_norm, float inv_sca
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, grad_clip_held_kernel<N>, t, meet, part, max_norm, inv_scale,
-                           (int32_t)(scale ? 1 : 0), norm, status) != cudaSuccess)
-      return MTGR_ERR_CUDA;
+    cudaLaunchKernelEx(&cfg, grad_clip_held_kernel<N>, t, meet, part, max_norm, inv_scale,
+                       (int32_t)(scale ? 1 : 0), norm, status);
     return launch_status();
   }
   for (int32_t i = 0; i < n; i += N) {
