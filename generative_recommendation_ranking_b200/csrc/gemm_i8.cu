@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(Epi<OUT, CG, KEEP_B>::kThreads, 1)
     int mb, nb;
     for (int i = 0; tile_at(i, mb, nb); ++i) {
       const int row0 = mb * S::kTileM + (int)rank * BM + quarter * 32;
-      const float sa = row0 + lane < M ? __ldg(args.sa + row0 + lane) : 0.f;
+      const float sa = row0 + lane < M ? load_written(args.sa + row0 + lane) : 0.f;
       const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase));
       if (!ok) { timed_out = true; break; }
       tc_fence_after();

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks)
   __syncthreads();
   if (!met) return;
   s = 0.0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += kHeldThreads) s += __ldcg(part + i);
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += kHeldThreads) s += load_written(part + i);
   s = block_sum(s);
   const double norm = sqrt(s) * (double)inv_scale;
   const bool finite = isfinite((float)norm);

@@ -16,6 +16,18 @@ namespace mtgr {
 // seen. The first one allows it as soon as all of its blocks run.
 __device__ __forceinline__ void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Reads what was written while this kernel ran, by the kernel before it or by another block: behind
+// the wait for it in the program, where __ldg (memory that never changes) may go ahead of it.
+__device__ __forceinline__ float load_written(const float* p) {
+  float v;
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ double load_written(const double* p) {
+  double v;
+  asm volatile("ld.relaxed.gpu.global.f64 %0, [%1];" : "=d"(v) : "l"(p) : "memory");
+  return v;
+}
 
 template <typename... P, typename... A>
 inline int launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,

@@ -487,6 +487,28 @@ def test_linear_is_quantise_then_product(M, dtype):
         assert torch.equal(mt.linear_i8(x, w, ws, bias=bias, epi=epi), mt.gemm_i8(q, s, w, ws, bias, epi))
 
 
+@pytest.mark.parametrize("M,N,K", [(9, 520, 512), (100, 1032, 4096), (1000, 1032, 512), (2500, 2048, 512), (2500, 1032, 2048)])
+def test_linear_from_inputs_that_change(M, N, K):
+    # in a graph: the product launches while its rows are quantised, and reads none of them before
+    w, ws = mt.quantize_rows(torch.randn(N, K, device="cuda"))
+    x = torch.randn(M, K, device="cuda")
+    out = torch.empty(M, N, device="cuda")
+    mt.linear_i8(x, w, ws, out_dtype=torch.float32, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mt.linear_i8(x, w, ws, out_dtype=torch.float32, out=out)
+    for k in range(4):
+        x.copy_(torch.randn(M, K, device="cuda") * (k + 1))
+        q, s = mt.quantize_rows(x)
+        want = mt.gemm_i8(q, s, w, ws, out_dtype=torch.float32)
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want), k
+        y = q.double() @ w.double().T * s.double()[:, None] * ws.double()
+        mag = (q.double() @ w.double().T).abs() * s.double()[:, None] * ws.double()
+        near(out, y.cpu().numpy(), mag.cpu().numpy(), "linear")
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 8, 16), (16, 72, 528), (17, 200, 64), (129, 520, 144), (9000, 1160, 512), (9001, 1000, 640)])
 @pytest.mark.parametrize("out", [torch.float32, torch.float16])
 def test_product_writes_its_rows_alone(M, N, K, out):
