@@ -14,7 +14,8 @@
 // 128 bytes in swizzled shared memory and leave them by TMA stores.
 //   CG = 2: CTA pairs, 256 x 256 tiles (an SM reads its 128 rows of a and half of
 //           the 256 columns of b): many rows.
-//   CG = 1: one CTA, 128 x 64 tiles, so that a few hundred rows spread over the SMs.
+//   CG = 1: one CTA, 128 x 64 tiles, so that a few hundred rows spread over the SMs;
+//           with a long k and too few of them, a cluster of CTAs for each (below).
 //   KEEP_B (pairs, k <= 512): a pair stays in its 256 columns and keeps their b in
 //           shared memory, which halves what L2 hands to the SMs.
 // Measured on one B200, bursts of 20: 8192^3 at 2.9-3.1 P op/s, where the operands'
@@ -534,6 +535,226 @@ int launch_cg(int M, int N, int K, const int8_t* a, const int8_t* b, int epi, in
   return MTGR_ERR_UNSUPPORTED;
 }
 
+// ------------------------------------------------ few tiles and a long k --
+// A cluster of `splits` CTAs shares one 128 x 64 tile: each multiplies its run of
+// k-blocks, leaves its int32 sums in its shared memory, and after a cluster barrier
+// finishes its share of the rows from all of theirs. Sums of integers: the
+// same bits as in one run over k.
+constexpr int kSplitK = 16;  // fewest k-blocks
+constexpr int kSplitThreads = 192, kSplitStages = 6;
+constexpr int kSplitRows = (BM / 2 * 8 + kSplitThreads - 1) / kSplitThreads;  // rows a thread finishes, at two splits
+constexpr size_t kSplitSmem = 1024 + (size_t)kSplitStages * Shape<1>::kStageBytes + 256;
+
+// 16-byte chunk c of row r of a tile of 64 int32 columns: chunks turned by the row, so that
+// eight rows' same chunk falls in different banks
+__device__ __forceinline__ uint32_t part_off(int r, int c) { return (uint32_t)(r * 256 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ int4 ld_peer(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+    gemm_i8_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, Args args,
+                         int splits, int epi, void* out) {
+  using S = Shape<1>;
+  constexpr int NST = kSplitStages, BN = S::kBN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + NST * A_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + NST * S::kBBytes);
+  uint64_t* empty = full + NST;
+  uint64_t* done = full + 2 * NST;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + 2 * NST + 1);
+
+  const int warp = warp_id(), lane = lane_id();
+  const int M = args.M, N = args.N;
+  const int n_tiles = (N + BN - 1) / BN, tile = (int)blockIdx.x / splits;
+  const int mb = tile / n_tiles, nb = tile - mb * n_tiles;
+  const int rank = (int)cluster_ctarank();
+  const int kblocks = (args.K + BK - 1) / BK;  // kSplitK at least
+  const int k0 = rank * kblocks / splits, k1 = (rank + 1) * kblocks / splits;
+
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, BN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  bool timed_out = false;
+  dependent_wait();  // a's bytes and scales may be another kernel's of the same call
+
+  // what finishing takes beside the sums, on its way while k is added up: the scales and the
+  // bias of a thread's eight columns (the same in each of its rows), its rows' scales
+  const int rows = BM / splits, n = nb * BN + 8 * (int)(threadIdx.x & 7);
+  float sb[8], bias[8], sa[kSplitRows];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    sb[e] = n < N ? __ldg(args.sb + n + e) : 0.f;  // N % 8 == 0
+    bias[e] = n < N && args.bias != nullptr ? __ldg(args.bias + n + e) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kSplitRows; ++i) {
+    const int r = i * (kSplitThreads / 8) + (int)(threadIdx.x >> 3), m = mb * BM + rank * rows + r;
+    sa[i] = r < rows && m < M ? load_written(args.sa + m) : 0.f;
+  }
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1)) { timed_out = true; break; }
+        mbar_arrive_expect_tx(&full[stage], S::kStageBytes);
+        tma_load_2d(&tmA, &full[stage], sA + stage * A_BYTES, kb * BK, mb * BM);
+        tma_load_2d(&tmB, &full[stage], sB + stage * S::kBBytes, kb * BK, nb * BN);
+        if (++stage == NST) { stage = 0; phase ^= 1; }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_i8(BM, BN);
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!mbar_wait(&full[stage], phase)) { timed_out = true; break; }
+        tc_fence_after();
+        const uint32_t a_addr = smem_u32(sA + stage * A_BYTES), b_addr = smem_u32(sB + stage * S::kBBytes);
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k)
+          mma_i8<1>(tmem_base, sdesc_sw128(a_addr + 32 * k, 16, 1024), sdesc_sw128(b_addr + 32 * k, 16, 1024), idesc,
+                    kb > k0 || k > 0 ? 1u : 0u);
+        tc_commit(&empty[stage]);
+        if (++stage == NST) { stage = 0; phase ^= 1; }
+      }
+      if (!timed_out) tc_commit(done);
+    }
+  } else {
+    // all multiplications done, so all loads landed: the stages of a take the sums
+    if (__all_sync(0xffffffffu, mbar_wait(done, 0))) {
+      tc_fence_after();
+      const int r = 32 * (warp & 3) + lane;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t v[32];
+        tmem_ld32(tmem_base + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 32 * half, v);
+        tmem_ld_wait();
+        reg_fence(v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(sA + part_off(r, 8 * half + c)) =
+              make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      }
+    } else {
+      timed_out = true;
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  // this CTA's rows of the tile, eight columns a thread
+  const int c = threadIdx.x & 7;
+#pragma unroll
+  for (int i = 0; i < kSplitRows; ++i) {
+    const int ri = i * (kSplitThreads / 8) + (int)(threadIdx.x >> 3), r = rank * rows + ri, m = mb * BM + r;
+    if (ri >= rows || m >= M || n >= N) continue;
+    int4 lo = make_int4(0, 0, 0, 0), hi = lo;
+#pragma unroll 4
+    for (int p = 0; p < splits; ++p) {
+      const uint32_t from = mapa_shared(sA, (uint32_t)p);
+      const int4 x = ld_peer(from + part_off(r, 2 * c)), y = ld_peer(from + part_off(r, 2 * c + 1));
+      lo.x += x.x; lo.y += x.y; lo.z += x.z; lo.w += x.w;
+      hi.x += y.x; hi.y += y.y; hi.z += y.z; hi.w += y.w;
+    }
+    const int s[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // rounded step by step, as in the other forms
+      v[e] = __fmul_rn(__int2float_rn(s[e]), __fmul_rn(sa[i], sb[e]));
+      if (args.bias != nullptr) v[e] = __fadd_rn(v[e], bias[e]);
+      if (epi == MTGR_EPI_SILU) v[e] = __fdividef(v[e], 1.0f + __expf(-v[e]));
+      if (epi == MTGR_EPI_RESID) v[e] = __fadd_rn(v[e], __ldg(args.resid + (size_t)m * N + n + e));
+      if (n < args.q_cols) v[e] = __fmul_rn(v[e], 0.5f);  // q_cols % 32 == 0
+    }
+    if (OUT == MTGR_F32) {
+      store8(static_cast<float*>(out) + (size_t)m * N + n, v);
+    } else if (OUT == MTGR_BF16) {
+      store8(static_cast<__nv_bfloat16*>(out) + (size_t)m * N + n, v);
+    } else {
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+      if (mx > 65504.f) set_status(args.status, MTGR_ERR_RANGE);
+      *reinterpret_cast<uint4*>(static_cast<__half*>(out) + (size_t)m * N + n) =
+          make_uint4(cvt_f16x2(v[0], v[1]), cvt_f16x2(v[2], v[3]), cvt_f16x2(v[4], v[5]), cvt_f16x2(v[6], v[7]));
+    }
+  }
+  if (timed_out) set_status(args.status, MTGR_ERR_TIMEOUT);
+  cluster_sync();  // no CTA ends while another reads its sums
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, BN);
+  }
+}
+
+template <int OUT>
+int launch_split_t(const CUtensorMap& ta, const CUtensorMap& tb, const Args& args, int tiles, int splits, int epi,
+                   void* out, cudaStream_t s, bool dependent) {
+  auto kern = gemm_i8_split_kernel<OUT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSplitSmem) != cudaSuccess)
+    return MTGR_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * splits));
+  cfg.blockDim = dim3(kSplitThreads);
+  cfg.dynamicSmemBytes = kSplitSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, kern, ta, tb, args, splits, epi, out);
+  return launch_status();
+}
+
+int launch_split(int M, int N, int K, const int8_t* a, const int8_t* b, int epi, int32_t out_dtype, void* out,
+                 const Args& args, int splits, cudaStream_t s, bool dependent) {
+  CUtensorMap ta, tb;
+  int rc = make_tmap_2d(&ta, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)M, (uint64_t)K, BK, BM,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != MTGR_OK) return rc;
+  rc = make_tmap_2d(&tb, b, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)N, (uint64_t)K, BK, Shape<1>::kBRows,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != MTGR_OK) return rc;
+  const int tiles = ((M + BM - 1) / BM) * ((N + Shape<1>::kBN - 1) / Shape<1>::kBN);
+  if (out_dtype == MTGR_F32) return launch_split_t<MTGR_F32>(ta, tb, args, tiles, splits, epi, out, s, dependent);
+  if (out_dtype == MTGR_BF16) return launch_split_t<MTGR_BF16>(ta, tb, args, tiles, splits, epi, out, s, dependent);
+  return launch_split_t<MTGR_F16>(ta, tb, args, tiles, splits, epi, out, s, dependent);
+}
+
 }  // namespace
 
 // K % 16 == 0, N % 8 == 0, 16-byte aligned operands.
@@ -547,6 +768,15 @@ int launch_gemm_i8(int M, int N, int K, const int8_t* a, const float* sa, const 
   // of them, 14.1 against 8.8.
   const int64_t small_tiles = (((int64_t)M + 127) / 128) * ((N + 63) / 64);
   if (small_tiles > 2 * device_sm_count()) return launch_cg<2>(M, N, K, a, b, epi, out_dtype, out, args, s, dependent);
+  // Few tiles and a long k: a cluster of two or four per tile, if the SMs hold them and k
+  // has kSplitK blocks. 100 x 1024 x 4096 takes 7.9 us in fours, 12.6 unsplit; 500 x 1024 x
+  // 4096, in twos, 10.3 against 12.9; 128 x 512 x 2048 6.8 against 8.1; but 300 x 1024 x
+  // 1024 6.7 against 6.0: the cluster and the exchange cost 1.2 us. Eights take 13.6 for
+  // the first (a cluster stays in its GPC, and sixteen of eight do not fit at once).
+  int splits = 4;
+  while (splits > 1 && small_tiles * splits > device_sm_count()) splits /= 2;
+  if ((K + BK - 1) / BK < kSplitK) splits = 1;
+  if (splits > 1) return launch_split(M, N, K, a, b, epi, out_dtype, out, args, splits, s, dependent);
   return launch_cg<1>(M, N, K, a, b, epi, out_dtype, out, args, s, dependent);
 }
 

@@ -454,6 +454,25 @@ def test_int8_product(M, N, K, epi, out):
     assert torch.isfinite(got).all()
 
 
+@pytest.mark.parametrize("M", [17, 64, 100, 128, 129, 257])
+@pytest.mark.parametrize("N,K", [(8, 512), (72, 528), (512, 1040), (1024, 4096), (1160, 2064), (264, 8208)])
+@pytest.mark.parametrize("epi,out", [("none", torch.float32), ("silu", torch.float16), ("silu", torch.bfloat16), ("resid", torch.float32)])
+def test_int8_product_split_over_k_is_the_same(M, N, K, epi, out):
+    # few tiles, k shared by a cluster: the same bits as these rows in a product of many
+    rng, many = torch.Generator(device="cuda").manual_seed(M + N + K), 10000
+    a, b = (torch.randint(-127, 128, (n, K), generator=rng, device="cuda", dtype=torch.int8) for n in (many, N))
+    sa, sb = ((torch.rand(n, generator=rng, device="cuda") + 0.5) / (73 * K ** 0.25) for n in (many, N))
+    bias, resid = (torch.randn(n, generator=rng, device="cuda") for n in ((N,), (many, N)))
+    q_cols = 32 if N >= 64 else 0
+    want = mt.gemm_i8(a, sa, b, sb, bias, EPIS[epi], resid if epi == "resid" else None, q_cols, out)
+    buf = torch.full((M + 300, N), 7.0, dtype=out, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mt.gemm_i8(a[:M], sa[:M], b, sb, bias, EPIS[epi], resid[:M] if epi == "resid" else None, q_cols, out,
+               out=buf[8:8 + M], status=status)
+    assert torch.equal(buf[8:8 + M], want[:M]) and (buf[:8] == 7).all() and (buf[8 + M:] == 7).all()
+    assert status.item() == 0
+
+
 def test_int8_product_extreme_sums_are_exact():
     # every byte -128: the sums pass 2^30; K close to the largest
     K = 131056
