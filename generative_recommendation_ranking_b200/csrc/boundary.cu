@@ -14,8 +14,9 @@
 //   b = dn gamma_post;  do = (b - mean b - ohat mean(b ohat)) / sigma_o
 //   dgamma_pre += dy hhat, dbeta_pre += dy, dgamma_post += dn ohat, dbeta_post += dn
 //
-// Both are bound by HBM: at bf16 branch, fp32 stream and bf16 y the forward moves
-// 14 bytes an element and the backward 22. Statistics, sums and gradients are
+// At bf16 branch, fp32 stream and bf16 y the forward moves 14 bytes an element, which
+// bounds it, and the backward 22; that one is bound by its instructions' latency from
+// d = 256 on, at two warps a scheduler (0.70 of the copy rate). Statistics, sums and gradients are
 // held in fp32 (the sums over rows in fp32 per run of rows, then in fp64); the
 // backward forms h again from x, o and u instead of reading a rounded one.
 #include <cuda_bf16.h>
