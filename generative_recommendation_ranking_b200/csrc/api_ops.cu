@@ -48,7 +48,7 @@ int gemm_i8_check(int32_t M, int32_t N, int32_t K, const void* b, const float* s
                   int32_t epi, const float* resid, int32_t q_cols, int32_t out_dtype, const void* out) {
   if (M < 0 || N < 0 || K <= 0 || q_cols < 0 || q_cols % 32 != 0) return MTGR_ERR_INVALID_ARG;
   if (epi != MTGR_EPI_NONE && epi != MTGR_EPI_SILU && epi != MTGR_EPI_RESID) return MTGR_ERR_INVALID_ARG;
-  if (epi == MTGR_EPI_RESID && out_dtype != MTGR_F32) return MTGR_ERR_INVALID_ARG;
+  if (epi == MTGR_EPI_RESID && (out_dtype != MTGR_F32 || (out != nullptr && resid == out))) return MTGR_ERR_INVALID_ARG;
   if (out_dtype != MTGR_F32 && out_dtype != MTGR_BF16 && out_dtype != MTGR_F16) return MTGR_ERR_UNSUPPORTED;
   if (K % 16 != 0 || N % 8 != 0 || K >= kMaxI8K || M > kMaxI8Rows || N > kMaxI8Rows) return MTGR_ERR_UNSUPPORTED;
   if (M > 0 && N > 0 &&

@@ -122,7 +122,7 @@ def test_int8_product_refusals(lib):
         for bad in (dict(M=-1), dict(N=-8), dict(K=0), dict(q_cols=-32), dict(q_cols=8), dict(epi=5), dict(b=None),
                     dict(sb=None), dict(out=None), dict(b=F + 8), dict(sb=F + 4), dict(bias=F + 4), dict(out=F + 8),
                     dict(epi=_lib.MTGR_EPI_RESID, od=F32), dict(epi=_lib.MTGR_EPI_RESID, resid=F),
-                    dict(epi=_lib.MTGR_EPI_RESID, resid=F + 4, od=F32)):
+                    dict(epi=_lib.MTGR_EPI_RESID, resid=F + 4, od=F32), dict(epi=_lib.MTGR_EPI_RESID, resid=F, od=F32)):
             assert f(**bad) == INVALID, (f.__name__, bad)
         assert f(M=(1 << 30) + 1) == UNSUPPORTED and f(N=(1 << 30) + 8) == UNSUPPORTED
         assert f(N=60) == UNSUPPORTED and f(od=I8) == UNSUPPORTED
