@@ -367,8 +367,9 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
   for (int j = 0; j < VPL; ++j) on[j] = c0 + j * VSTEP < d;
   const int64_t t0 = ti * a.rows_per_team;
   const int rows = ti < a.teams ? (int)min((int64_t)a.rows_per_team, (int64_t)a.T - t0) : 0;
-  // the warp's teams go through the loop together: one whose rows are done goes on
-  // with rows of zeros, which add nothing, and stores nothing
+  // the warp's teams go through the loop together: one whose rows are done leaves its
+  // sums, goes on with rows of zeros and keeps nothing of them (with eps = 0 their 1 / sigma
+  // is infinite, and what they add NaN)
   const int most = LANES == 32 ? rows : (int)__reduce_max_sync(0xffffffffu, (unsigned)rows);
   const bool post = a.post_gamma != nullptr, pre = a.pre_gamma != nullptr, gate = a.gate != MTGR_GATE_NONE;
   const float inv_d = 1.0f / (float)d;
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
     const bool live = LANES == 32 || r < rows;
     copy_row(r + AHEAD, s == 0 ? AHEAD : s - 1);  // stage (s + AHEAD) mod (AHEAD + 1)
     const int g_next = r + 1 < rows ? clamp_group(a.gid, t0 + r + 1, a.G) : g;
-    if (g != g_run) {
+    if (g != g_run || (LANES < 32 && r == rows)) {
       flush();
       g_run = g;
       take_params(g);
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS, bwd_blocks(WARP
     g = g_next;
     s = s == AHEAD ? 0 : s + 1;
   }
-  flush();
+  if (rows == most) flush();  // the others left theirs when their rows were done
   if (tl == 0 && ti < a.teams) a.seen[ti] = seen;
   if (range_bad) set_status(a.status, MTGR_ERR_RANGE);
 }
