@@ -3,7 +3,10 @@
 Each function checks shapes, types and places of its tensors, allocates the
 outputs that are not given (and the workspace), and makes one call into the C
 ABI on ``stream`` (default: the device's current stream). What it allocates is
-tied to ``stream``, so it may be dropped while the work still runs.
+``stream``'s own memory, so nothing that still runs on another stream uses it, and
+it may be dropped while the work runs on ``stream`` or its results are read on the
+current stream. The order between the two streams is the caller's: inputs ready for
+``stream`` before the call, results read behind it.
 """
 
 from __future__ import annotations
@@ -56,18 +59,23 @@ def _where(stream, dev: int):
     return stream.cuda_stream, stream
 
 
-def _new(like, other, shape=None, dtype=None) -> torch.Tensor:
-    """A buffer beside ``like``, of its shape and type unless given: the allocator
-    counts it to the current stream, so one on another stream is recorded there.
-    (An existing tensor's allocation is called twice as fast as torch.empty.)"""
-    if shape is None:
-        t = torch.empty_like(like, memory_format=_DENSE) if dtype is None else \
-            torch.empty_like(like, dtype=dtype, memory_format=_DENSE)
-    else:
-        t = like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+def _new(like, other, shape=None, dtype=None, scratch=False) -> torch.Tensor:
+    """A buffer beside ``like``, of its shape and type unless given. One for another
+    stream comes out of that stream's memory (the current stream's may be a buffer that
+    was dropped while its work there still runs), and unless it is scratch, is kept from
+    being handed out again before the current stream, where its reader is, has got past
+    its release. (An existing tensor's allocation is called twice as fast as torch.empty.)"""
     if other is not None:
-        t.record_stream(other)
-    return t
+        now = torch.cuda.current_stream(like.device)
+        with torch.cuda.stream(other):
+            t = _new(like, None, shape, dtype)
+        if not scratch:
+            t.record_stream(now)
+        return t
+    if shape is None:
+        return torch.empty_like(like, memory_format=_DENSE) if dtype is None else \
+            torch.empty_like(like, dtype=dtype, memory_format=_DENSE)
+    return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
 
 
 def _given(name: str, t, shape, dtype, dev: int) -> None:
@@ -222,7 +230,7 @@ def boundary_backward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=
     need = _lib.load().mtgr_boundary_bwd_workspace_bytes(T, _byref(p))
     if ws is None or ws.numel() * ws.element_size() < need:
         room = max(need, 256)
-        ws = _new(group_id, other, room)
+        ws = _new(group_id, other, room, scratch=True)
     else:
         room = ws.numel() * ws.element_size()
     _lib.check("mtgr_boundary_bwd", _lib.load().mtgr_boundary_bwd(
@@ -307,7 +315,7 @@ def linear_i8(x, w, w_scale, x_scale=None, bias=None, epi: int = MTGR_EPI_NONE, 
     if need == 0:
         p, room = None, 0
     elif ws is None or ws.numel() * ws.element_size() < need:
-        ws = _new(w, other, need)
+        ws = _new(w, other, need, scratch=True)
         p, room = ws.data_ptr(), need
     else:
         p, room = ws.data_ptr(), ws.numel() * ws.element_size()

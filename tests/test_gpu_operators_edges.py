@@ -37,3 +37,112 @@ def test_boundary_forward_without_eps(d):
     m = mags(r, "linear")
     near(h, want[0], 1.001 * m["h"], "h")
     near(y, want[1], 1.001 * m["y"], "y")
+
+
+# ----------------------------------------------------------------- streams --
+def stream_calls():
+    """Each operator that allocates, on fixed inputs: its outputs on a stream."""
+    dev, _ = case(3000, 512)
+    dh, dy = upstream(3000, 512)
+    w, ws = mt.quantize_rows(torch.randn(1024, 512, device="cuda"))
+    x = torch.randn(3000, 512, device="cuda")
+    q, s = mt.quantize_rows(x)
+    plan = mt.GradientSet([torch.randn(100003, device="cuda")], [torch.empty(100003, device="cuda")])
+    return {
+        "forward": lambda st: mt.boundary_forward(**dev, y_dtype=torch.int8, stream=st),
+        "backward": lambda st: tuple(mt.boundary_backward(**dev, dh=dh, dy=dy, stream=st).values()),
+        "quantise": lambda st: mt.quantize_rows(x, stream=st),
+        "product": lambda st: (mt.gemm_i8(q, s, w, ws, stream=st),),
+        "linear": lambda st: (mt.linear_i8(x, w, ws, stream=st),),
+        "linear, few rows": lambda st: (mt.linear_i8(x[:9], w, ws, stream=st),),
+        "clip": lambda st: (plan.clip(0.5, stream=st), *plan.outs),
+        "norm": lambda st: (plan.norm(stream=st),),
+    }
+
+
+STREAM_CALLS = ["forward", "backward", "quantise", "product", "linear", "linear, few rows", "clip", "norm"]
+
+
+def outputs_alone(name, got):
+    return got[:1] if name == "clip" else got  # what the call allocates
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_another_streams_buffers_are_no_dropped_ones(name):
+    # a kernel of the current stream is still to write buffers that were dropped: a call on
+    # another stream, which nothing orders behind it, gets none of them
+    call = stream_calls()[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    junk = [torch.empty_like(t) for t in want for _ in range(4)]
+    junk += [torch.empty(n << 20, dtype=torch.uint8, device="cuda") for n in (1, 2, 4, 8, 16, 32, 64)]  # workspaces
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about 0.1 s
+    for t in junk:
+        t.view(torch.uint8).fill_(0x55)
+    del junk, t
+    got = call(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_dropped_results_wait_for_their_reader(name):
+    # results read on the current stream, dropped before that has run: the next call on the
+    # other stream does not get their memory
+    call = stream_calls()[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    now = torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    got = outputs_alone(name, list(call(side)))
+    now.wait_stream(side)
+    side.synchronize()
+    torch.cuda._sleep(200_000_000)
+    keep = [t.clone() for t in got]
+    del got
+    with torch.cuda.stream(side):
+        junk = [torch.empty_like(t).view(torch.uint8).fill_(0x55) for t in keep for _ in range(4)]
+    again = outputs_alone(name, call(side))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, keep)) and all(torch.equal(a, b) for a, b in zip(want, again))
+    del junk
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_on_a_side_stream_of_a_capture(name):
+    call = stream_calls()[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        now = torch.cuda.current_stream()
+        side.wait_stream(now)
+        got = call(side)
+        now.wait_stream(side)
+        copies = [t.clone() for t in got]
+    for _ in range(3):
+        for t in copies:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, copies))
+
+
+def test_workspaces_of_another_stream_are_used_again():
+    # no reader on the current stream: a workspace does not wait for what runs there
+    w, ws = mt.quantize_rows(torch.randn(1024, 512, device="cuda"))
+    x, out = torch.randn(30000, 512, device="cuda"), torch.empty(30000, 1024, device="cuda")
+    side = torch.cuda.Stream()
+    mt.linear_i8(x, w, ws, out=out, stream=side)
+    torch.cuda.synchronize()
+    room = torch.cuda.memory_reserved()
+    torch.cuda._sleep(200_000_000)
+    for _ in range(20):
+        mt.linear_i8(x, w, ws, out=out, stream=side)
+    assert torch.cuda.memory_reserved() == room
+    torch.cuda.synchronize()
