@@ -126,9 +126,10 @@ __device__ __forceinline__ void load_cols(const float* p, int col0, int N, float
 
 // The scales, bias and epilogue of 32 columns [col0, col0 + 32) of one row whose
 // TMEM load is under way: the column scales' loads run beside it, `loaded` when it
-// is done. The result goes to chunks [c0, ...) of row r of the staging block.
+// is done. The result goes to chunks [c0, ...) of row r of the staging block. live: a row
+// of the output; one behind the last is not stored and, of the bias alone, reports no range.
 template <int EPI, int OUT, bool FULL, typename Loaded>
-__device__ __forceinline__ void epilogue_cols(const Args& a, int col0, float sa, uint32_t (&acc)[32],
+__device__ __forceinline__ void epilogue_cols(const Args& a, int col0, float sa, bool live, uint32_t (&acc)[32],
                                               const float4 (&res)[8], uint8_t* stg, int r, int c0,
                                               Loaded loaded) {
   float4 sb[8];
@@ -194,7 +195,7 @@ __device__ __forceinline__ void epilogue_cols(const Args& a, int col0, float sa,
         float mx = 0.f;
 #pragma unroll
         for (int c = 0; c < 32; ++c) mx = fmaxf(mx, fabsf(v[c]));
-        if (mx > 65504.f) set_status(a.status, MTGR_ERR_RANGE);
+        if (live && mx > 65504.f) set_status(a.status, MTGR_ERR_RANGE);
       }
     }
   }
@@ -383,7 +384,8 @@ __global__ void __launch_bounds__(Epi<OUT, CG, KEEP_B>::kThreads, 1)
     int mb, nb;
     for (int i = 0; tile_at(i, mb, nb); ++i) {
       const int row0 = mb * S::kTileM + (int)rank * BM + quarter * 32;
-      const float sa = row0 + lane < M ? load_written(args.sa + row0 + lane) : 0.f;
+      const bool live = row0 + lane < M;
+      const float sa = live ? load_written(args.sa + row0 + lane) : 0.f;
       const bool ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase));
       if (!ok) { timed_out = true; break; }
       tc_fence_after();
@@ -420,9 +422,9 @@ __global__ void __launch_bounds__(Epi<OUT, CG, KEEP_B>::kThreads, 1)
             tmem_ld32(t_row + blk * E::kCols + 32 * half, r);
             const auto loaded = [&] { if (end) release(); };
             if (col + 32 <= N)
-              epilogue_cols<EPI, OUT, true>(args, col, sa, r, rs[cc % RB], st, lane, 4 * half, loaded);
+              epilogue_cols<EPI, OUT, true>(args, col, sa, live, r, rs[cc % RB], st, lane, 4 * half, loaded);
             else
-              epilogue_cols<EPI, OUT, false>(args, col, sa, r, rs[cc % RB], st, lane, 4 * half, loaded);
+              epilogue_cols<EPI, OUT, false>(args, col, sa, live, r, rs[cc % RB], st, lane, 4 * half, loaded);
           }
           fence_proxy_async_smem();
           __syncwarp();

@@ -146,3 +146,23 @@ def test_workspaces_of_another_stream_are_used_again():
         mt.linear_i8(x, w, ws, out=out, stream=side)
     assert torch.cuda.memory_reserved() == room
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------ int8 product --
+@pytest.mark.parametrize("M,N,K", [(9, 72, 512), (17, 64, 512), (100, 64, 512), (100, 64, 4096), (1001, 328, 512), (9001, 2048, 512), (9001, 2048, 528)])
+@pytest.mark.parametrize("out", [torch.float32, torch.float16])
+def test_range_is_that_of_the_rows(M, N, K, out):
+    # a bias beyond f16 that every row's product brings back into it: the rows a tile has
+    # behind the last, of the bias alone, say nothing
+    a = torch.full((M, K), 100, dtype=torch.int8, device="cuda")
+    b = torch.full((N, K), -100, dtype=torch.int8, device="cuda")
+    one, bias = torch.ones(N, device="cuda"), torch.full((N,), 1e5, device="cuda")
+    sa = torch.full((M,), 9e4 / (K * 1e4), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mt.gemm_i8(a, sa, b, one, bias, out_dtype=out, status=status)
+    assert status.item() == 0
+    # -9e4 + 1e5 with three roundings near 1e5, then one to the output's type
+    assert ((got.double() - 1e4).abs() <= 3 * 1e5 * 2.0 ** -24 + 1e4 * 2.0 ** -11).all()
+    sa[M - 1] = 0.0  # the last row of the output is the bias
+    mt.gemm_i8(a, sa, b, one, bias, out_dtype=out, status=status)
+    assert status.item() == (mt._lib.MTGR_ERR_RANGE if out == torch.float16 else 0)
