@@ -186,8 +186,10 @@ template <typename TX>
 int launch_t(const FewArgs& a, int epi, int32_t out_dtype, cudaStream_t s) {
   const int bytes = smem_bytes(a.K);
   auto kern = gemm_i8_few_kernel<TX>;
+  // always the largest: a limit set to this call's bytes could fall below what another
+  // thread, between its own setting and its launch, is about to ask for
   if (bytes > 40 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRowsBytes) != cudaSuccess)
     return MTGR_ERR_CUDA;
   kern<<<(a.N + kCols - 1) / kCols, 32 * kWarps, bytes, s>>>(a, epi, out_dtype);
   return launch_status();

@@ -1,6 +1,8 @@
 """The operators' calls beside the ordinary ones, each against the float64 oracle or
 against the same call made plainly. Tolerances: tests/test_gpu_operators.py."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -166,3 +168,29 @@ def test_range_is_that_of_the_rows(M, N, K, out):
     sa[M - 1] = 0.0  # the last row of the output is the bias
     mt.gemm_i8(a, sa, b, one, bias, out_dtype=out, status=status)
     assert status.item() == (mt._lib.MTGR_ERR_RANGE if out == torch.float16 else 0)
+
+
+def test_few_rows_from_several_threads():
+    # calls of two lengths of k at once, each with its own shared memory: none is refused
+    # (60,000 calls in each of four threads: some dozens were where the threads' limits mixed)
+    f = mt.load().mtgr_linear_i8
+    refused, outs = [], []
+
+    def work(K):
+        x = torch.randn(8, K, device="cuda")
+        w = torch.ones(16, K, dtype=torch.int8, device="cuda")
+        scale, out = torch.ones(16, device="cuda"), torch.empty(8, 16, device="cuda")
+        torch.cuda.synchronize()
+        stream = torch.cuda.Stream()
+        args = (8, 16, K, mt.MTGR_F32, x.data_ptr(), K, w.data_ptr(), scale.data_ptr(), None, 0, None, 0, mt.MTGR_F32,
+                out.data_ptr(), None, 0, None, stream.cuda_stream)
+        refused.append(sum(f(*args) != 0 for _ in range(60000)))
+        stream.synchronize()
+        outs.append(torch.equal(out, mt.linear_i8(x, w, scale)))
+
+    threads = [threading.Thread(target=work, args=(K,)) for K in (2816, 6016, 2816, 6016)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert refused == [0] * 4 and outs == [True] * 4
