@@ -156,12 +156,14 @@ __global__ void __launch_bounds__(32 * kWarps) gemm_i8_few_kernel(FewArgs a, int
     int s = 0;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) s += part[k * kRows * kCols + i];
-    float v = __int2float_rn(s) * (row_s[m] * a.sb[n]);
-    if (a.bias != nullptr) v += a.bias[n];
+    // rounded step by step, as in the other forms: a row's bits do not depend on how many
+    // rows share the call
+    float v = __fmul_rn(__int2float_rn(s), __fmul_rn(row_s[m], a.sb[n]));
+    if (a.bias != nullptr) v = __fadd_rn(v, a.bias[n]);
     if (epi == MTGR_EPI_SILU) v = __fdividef(v, 1.0f + __expf(-v));
     const int64_t at = (int64_t)m * a.N + n;
-    if (epi == MTGR_EPI_RESID) v += a.resid[at];
-    if (n < a.q_cols) v *= 0.5f;
+    if (epi == MTGR_EPI_RESID) v = __fadd_rn(v, a.resid[at]);
+    if (n < a.q_cols) v = __fmul_rn(v, 0.5f);
     if (out_dtype == MTGR_F32) {
       static_cast<float*>(a.out)[at] = v;
     } else if (out_dtype == MTGR_BF16) {

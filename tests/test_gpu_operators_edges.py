@@ -9,7 +9,7 @@ import torch
 
 import generative_recommendation_ranking_b200 as mt
 from oracle import operators as op
-from test_gpu_operators import case, host, mags, near, oracle_args, upstream
+from test_gpu_operators import EPIS, case, host, mags, near, oracle_args, product_case, upstream
 
 pytestmark = pytest.mark.gpu
 
@@ -194,3 +194,23 @@ def test_few_rows_from_several_threads():
     for t in threads:
         t.join()
     assert refused == [0] * 4 and outs == [True] * 4
+
+
+@pytest.mark.parametrize("N,K", [(8, 16), (72, 528), (328, 512), (2048, 512), (1024, 4096)])
+@pytest.mark.parametrize("epi,out", [("none", torch.float32), ("none", torch.float16), ("silu", torch.float32),
+                                     ("silu", torch.bfloat16), ("resid", torch.float32)])
+def test_a_rows_bits_do_not_depend_on_the_rows_beside_it(N, K, epi, out):
+    # one to sixteen rows take one form, the others tiles of one or two CTAs, or k in shares
+    a, sa, b, sb, bias, resid = (torch.from_numpy(v).cuda() for v in product_case(10007, N, K))
+    x = torch.randn(10007, K, device="cuda")
+    q_cols = 32 if N >= 64 else 0
+
+    def both(n):
+        more = (b, sb, bias, EPIS[epi], resid[:n] if epi == "resid" else None, q_cols, out)
+        return mt.gemm_i8(a[:n], sa[:n], *more), mt.linear_i8(x[:n], *more[:2], bias=more[2], epi=more[3], resid=more[4],
+                                                             q_cols=more[5], out_dtype=more[6])
+
+    want = both(10007)
+    for n in (1, 2, 15, 16, 17, 129, 1000):
+        for g, v in zip(both(n), want):
+            assert torch.equal(g, v[:n]), n
