@@ -26,6 +26,7 @@
 
 #include "common.cuh"
 #include "ops.h"
+#include "row_runs.h"
 #include "rowvec.cuh"
 
 namespace mtgr {
@@ -284,8 +285,6 @@ int launch_fwd_t(const BoundaryFwdArgs& a, cudaStream_t s) {
 }
 
 // --------------------------------------------------------------- backward --
-// Gradient slots of the workspace, per team and group.
-constexpr int kSlots = 5;
 enum { kPreGamma = 0, kPreBeta = 1, kScale = 2, kPostGamma = 3, kPostBeta = 4 };
 
 // A row's inputs wait in shared memory: each thread copies its own eight values of
@@ -729,19 +728,6 @@ __global__ void __launch_bounds__(512) boundary_bwd_reduce_kernel(BoundaryBwdArg
   if (to != nullptr) to[(int64_t)(gs2 / kSlots) * a.d + (cc - (int64_t)gs2 * a.d)] = (float)t;
 }
 
-// Teams of the backward: at most `resident`, at least 4 rows each, and at most
-// 256 MB of gradient slots.
-int32_t bwd_teams(int32_t T, int32_t d, int32_t G, int64_t resident) {
-  if (T <= 0) return 0;
-  int64_t teams = resident;
-  const int64_t most = (256ll << 20) / ((int64_t)G * kSlots * d * 4);
-  if (teams > most) teams = most > 0 ? most : 1;
-  const int64_t by_rows = ((int64_t)T + 3) / 4;
-  if (teams > by_rows) teams = by_rows;
-  const int64_t rows = ((int64_t)T + teams - 1) / teams;
-  return (int32_t)(((int64_t)T + rows - 1) / rows);
-}
-
 // Warps of a row's team and vectors a thread.
 inline int bwd_warps(int d) { return d <= 512 ? 1 : (d <= 1024 ? 2 : (d <= 2048 ? 4 : (d <= 4096 ? 8 : 16))); }
 inline int bwd_vpl(int d) { return d <= 256 ? 1 : 2; }
@@ -766,7 +752,7 @@ int launch_bwd_w(BoundaryBwdArgs& a, cudaStream_t s) {
   constexpr int blocks = by_regs < by_smem ? by_regs : by_smem;
   constexpr int per_block = WARPS == 1 ? 128 / LANES : 1;
   a.teams = bwd_teams(a.T, a.d, a.G, (int64_t)device_sm_count() * blocks * per_block);
-  a.rows_per_team = (a.T + a.teams - 1) / a.teams;
+  a.rows_per_team = rows_per_team(a.T, a.teams);
   auto kern = boundary_bwd_kernel<TO, TX, WARPS, LANES, VPL>;
   if (bytes > 40 * 1024 &&  // 48 KB without asking, some of it static
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)

@@ -1,0 +1,42 @@
+"""Host arithmetic and refusals of the operators at their limits, on the CPU."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "generative_recommendation_ranking_b200", "csrc")
+
+RUNS = r"""
+#include <stdio.h>
+#include <initializer_list>
+#include "row_runs.h"
+int main() {
+  const int32_t T[] = {1, 3, 4, 5, 1917, 20011, 200003, 1 << 30, 2147481600, 2147483646, 2147483647};
+  const int64_t resident[] = {1, 148, 1184, 7104, 14208};
+  for (int32_t t : T)
+    for (int64_t r : resident)
+      for (int32_t d : {8, 64, 512, 8192})
+        for (int32_t G : {1, 4, 32}) {
+          const int32_t n = mtgr::bwd_teams(t, d, G, r);
+          printf("%d %lld %d %d %d %d\n", t, (long long)r, d, G, n, mtgr::rows_per_team(t, n));
+        }
+}
+"""
+
+
+def test_rows_are_dealt_out_up_to_the_largest_count(tmp_path):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        pytest.skip("no C++ compiler")
+    (tmp_path / "runs.cc").write_text(RUNS)
+    subprocess.run([cxx, "-std=c++17", "-fwrapv", "-Wall", "-Werror", "-I", CSRC, str(tmp_path / "runs.cc"), "-o",
+                    str(tmp_path / "runs")], check=True)
+    out = subprocess.run([str(tmp_path / "runs")], capture_output=True, text=True, check=True).stdout
+    for line in out.splitlines():
+        T, resident, d, G, teams, rows = map(int, line.split())
+        # every row has one team, and every team a row; slots of at most 256 MB, unless one team
+        assert teams >= 1 and rows >= 1 and teams * rows >= T > (teams - 1) * rows, line
+        assert teams <= resident and (teams == 1 or teams * G * 5 * d * 4 <= 256 << 20), line
