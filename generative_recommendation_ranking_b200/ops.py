@@ -84,6 +84,17 @@ def _given(name: str, t, shape, dtype, dev: int) -> None:
                          f"{tuple(t.shape)} of {t.dtype} on {t.device}, strides {t.stride()}")
 
 
+def _given_ws(ws, need: int, dev: int) -> int:
+    """Bytes of a workspace that the caller gave; 0 if it is too small, or none."""
+    if ws is None:
+        return 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: contiguous memory on cuda:{dev} is needed, got {tuple(ws.shape)} of {ws.dtype} on "
+                         f"{ws.device}, strides {ws.stride()}")
+    room = ws.numel() * ws.element_size()
+    return room if room >= need else 0
+
+
 def _given_rows(name: str, t, shape, dtypes, dev: int) -> int:
     """Checks a tensor whose rows may be further apart than their length; returns
     how far (that of a single row means nothing)."""
@@ -228,11 +239,10 @@ def boundary_backward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=
                 ptr[i] = base + 4 * k * p.G * d
                 k += 1
     need = _lib.load().mtgr_boundary_bwd_workspace_bytes(T, _byref(p))
-    if ws is None or ws.numel() * ws.element_size() < need:
+    room = _given_ws(ws, need, dev)
+    if room == 0:
         room = max(need, 256)
         ws = _new(group_id, other, room, scratch=True)
-    else:
-        room = ws.numel() * ws.element_size()
     _lib.check("mtgr_boundary_bwd", _lib.load().mtgr_boundary_bwd(
         _byref(p), T, group_id.data_ptr(), _CODE[o.dtype], o.data_ptr(), ld_o, u.data_ptr() if ld_u else None, ld_u,
         _CODE[x.dtype], x.data_ptr(), None if dh is None else dh.data_ptr(), 0 if dy is None else _CODE[dy.dtype],
@@ -312,13 +322,11 @@ def linear_i8(x, w, w_scale, x_scale=None, bias=None, epi: int = MTGR_EPI_NONE, 
         raise ValueError("x_scale goes with int8 rows")
     ld = _given_rows("x", x, (M, K), _FLOATS, dev)
     need = _lib.load().mtgr_linear_i8_workspace_bytes(M, N, K)
-    if need == 0:
-        p, room = None, 0
-    elif ws is None or ws.numel() * ws.element_size() < need:
-        ws = _new(w, other, need, scratch=True)
-        p, room = ws.data_ptr(), need
-    else:
-        p, room = ws.data_ptr(), ws.numel() * ws.element_size()
+    room, p = _given_ws(ws, need, dev), None
+    if need > 0:
+        if room == 0:
+            ws, room = _new(w, other, need, scratch=True), need
+        p = ws.data_ptr()
     _lib.check("mtgr_linear_i8", _lib.load().mtgr_linear_i8(M, N, K, _CODE[x.dtype], x.data_ptr(), ld, *tail, p, room, st,
                                                             raw))
     return out

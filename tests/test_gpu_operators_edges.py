@@ -214,3 +214,20 @@ def test_a_rows_bits_do_not_depend_on_the_rows_beside_it(N, K, epi, out):
     for n in (1, 2, 15, 16, 17, 129, 1000):
         for g, v in zip(both(n), want):
             assert torch.equal(g, v[:n]), n
+
+
+# -------------------------------------------------------------- workspaces --
+def test_given_workspaces():
+    dev, _ = case(300, 256)
+    dh, dy = upstream(300, 256)
+    x, (w, ws) = torch.randn(300, 256, device="cuda"), mt.quantize_rows(torch.randn(64, 256, device="cuda"))
+    want = mt.boundary_backward(**dev, dh=dh, dy=dy)
+    calls = (lambda b: mt.boundary_backward(**dev, dh=dh, dy=dy, ws=b)["scale"], lambda b: mt.linear_i8(x, w, ws, ws=b))
+    for call, ref in zip(calls, (want["scale"], mt.linear_i8(x, w, ws))):
+        for bad in (torch.zeros(1 << 24, dtype=torch.uint8), torch.zeros(1 << 25, dtype=torch.uint8, device="cuda")[::2]):
+            with pytest.raises(ValueError):
+                call(bad)
+        for good in (None, torch.zeros(1 << 22, device="cuda"), torch.zeros(16, device="cuda")):  # the last is too small
+            assert torch.equal(call(good), ref)
+    with pytest.raises(ValueError):  # checked for few rows, too, which need none
+        mt.linear_i8(x[:4], w, ws, ws=torch.zeros(64, dtype=torch.uint8))

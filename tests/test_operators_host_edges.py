@@ -5,6 +5,9 @@ import shutil
 import subprocess
 
 import pytest
+import torch
+
+from generative_recommendation_ranking_b200 import ops
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "generative_recommendation_ranking_b200", "csrc")
@@ -40,3 +43,16 @@ def test_rows_are_dealt_out_up_to_the_largest_count(tmp_path):
         # every row has one team, and every team a row; slots of at most 256 MB, unless one team
         assert teams >= 1 and rows >= 1 and teams * rows >= T > (teams - 1) * rows, line
         assert teams <= resident and (teams == 1 or teams * G * 5 * d * 4 <= 256 << 20), line
+
+
+def test_a_given_workspace_is_checked():
+    # a host tensor's device is -1: one that is asked for on the GPU is refused before its
+    # address is used, and so is one with gaps, between which others' bytes lie
+    whole = torch.zeros(1024, dtype=torch.uint8)
+    assert ops._given_ws(None, 100, 0) == 0
+    for dev, ws in ((0, whole), (-1, whole[::2]), (-1, whole.view(32, 32)[:, :16]), (-1, whole.view(32, 32).t())):
+        with pytest.raises(ValueError, match="ws"):
+            ops._given_ws(ws, 100, dev)
+    assert ops._given_ws(whole, 1024, -1) == 1024 and ops._given_ws(whole, 1025, -1) == 0
+    assert ops._given_ws(whole[512:], 100, -1) == 512 and ops._given_ws(torch.zeros(8, 8), 100, -1) == 256
+    assert ops._given_ws(whole[:0], 0, -1) == 0
