@@ -473,6 +473,10 @@ def mtgr_stack_fwd_host(layers, h_lens, h_ts, h_norm, h_x_in, h_x_out, h_status,
         d_ws.numel() * d_ws.element_size(), _stream(stream)))
 
 
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
 def _i8_dtype(t: torch.dtype) -> int:
     return MTGR_I8 if t == torch.int8 else dtype_code(t)
 
@@ -498,7 +502,7 @@ def mtgr_boundary_bwd(p: MtgrBoundaryParams, T, d_group_id, d_o, d_u, d_x, d_dh,
         _ptr(d_u), 0 if d_u is None else d_u.stride(0), dtype_code(d_dx.dtype), _ptr(d_x),
         _ptr(d_dh), MTGR_F32 if d_dy is None else dtype_code(d_dy.dtype), _ptr(d_dy), _ptr(d_do),
         d_do.stride(0), _ptr(d_du), 0 if d_du is None else d_du.stride(0), _ptr(d_dx),
-        ctypes.byref(grads), _ptr(d_ws), d_ws.numel() * d_ws.element_size(), _ptr(d_status),
+        ctypes.byref(grads), _ptr(d_ws), _bytes(d_ws), _ptr(d_status),
         _stream(stream)))
 
 
@@ -524,11 +528,12 @@ def mtgr_linear_i8_workspace_bytes(M: int, N: int, K: int) -> int:
 
 def mtgr_linear_i8(d_x, d_w, d_w_scale, d_bias, epi, d_resid, q_cols, d_out, d_ws, d_status,
                    stream=None) -> None:
+    """d_ws None where mtgr_linear_i8_workspace_bytes is 0."""
     M, K = d_x.shape
     _check("mtgr_linear_i8", load().mtgr_linear_i8(
         M, d_w.shape[0], K, dtype_code(d_x.dtype), _ptr(d_x), d_x.stride(0), _ptr(d_w),
         _ptr(d_w_scale), _ptr(d_bias), epi, _ptr(d_resid), q_cols, dtype_code(d_out.dtype),
-        _ptr(d_out), _ptr(d_ws), d_ws.numel() * d_ws.element_size(), _ptr(d_status),
+        _ptr(d_out), _ptr(d_ws), _bytes(d_ws), _ptr(d_status),
         _stream(stream)))
 
 
@@ -541,4 +546,4 @@ def mtgr_grad_clip(h_grads, n: int, max_norm: float, inv_scale: float, d_norm, d
                    stream=None) -> None:
     _check("mtgr_grad_clip", load().mtgr_grad_clip(
         h_grads, n, max_norm, inv_scale, _ptr(d_norm), _ptr(d_ws),
-        d_ws.numel() * d_ws.element_size(), _ptr(d_status), _stream(stream)))
+        _bytes(d_ws), _ptr(d_status), _stream(stream)))

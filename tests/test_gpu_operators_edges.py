@@ -231,3 +231,42 @@ def test_given_workspaces():
             assert torch.equal(call(good), ref)
     with pytest.raises(ValueError):  # checked for few rows, too, which need none
         mt.linear_i8(x[:4], w, ws, ws=torch.zeros(64, dtype=torch.uint8))
+
+
+def test_the_entry_points_one_by_one():
+    # the binding's wrappers of the library's entry points, on the caller's buffers
+    L = mt._lib
+    dev, _ = case(40, 264, gate="silu")
+    names = ("post_gamma", "post_beta", "scale", "pre_gamma", "pre_beta")
+    p = L.MtgrBoundaryParams(264, 4, 1e-5, L.MTGR_GATE_SILU, *[dev[n].data_ptr() for n in names])
+    h, y, ys = torch.empty(40, 264, device="cuda"), torch.empty(40, 264, dtype=torch.int8, device="cuda"), torch.empty(40, device="cuda")
+    mt.mtgr_boundary_fwd(p, 40, dev["group_id"], dev["o"], dev["u"], dev["x"], h, y, ys)
+    want = mt.boundary_forward(**dev, gate="silu", y_dtype=torch.int8)
+    assert all(torch.equal(a, b) for a, b in zip((h, y, ys), want))
+    # no rows: no workspace
+    none = {k: (v[:0] if k in ("x", "o", "u", "group_id") else v) for k, v in dev.items()}
+    grads = {n: torch.full((4, 264), 7.0, device="cuda") for n in names}
+    mt.mtgr_boundary_bwd(p, 0, none["group_id"], none["o"], none["u"], none["x"], None, none["x"], none["o"], none["o"], none["x"],
+                         L.MtgrBoundaryGrads(*[grads[n].data_ptr() for n in names]), None)
+    assert all((g == 0).all() for g in grads.values())
+    x = torch.randn(40, 272, device="cuda")
+    q, s = torch.empty(40, 272, dtype=torch.int8, device="cuda"), torch.empty(40, device="cuda")
+    mt.mtgr_quantize_rows(x, q, s)
+    assert all(torch.equal(a, b) for a, b in zip((q, s), mt.quantize_rows(x)))
+    w, ws = mt.quantize_rows(torch.randn(72, 272, device="cuda"))
+    out, status = torch.empty(40, 72, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    mt.mtgr_gemm_i8(q, s, w, ws, None, mt.MTGR_EPI_SILU, None, 0, out, status)
+    ref = mt.gemm_i8(q, s, w, ws, epi=mt.MTGR_EPI_SILU)
+    assert torch.equal(out, ref)
+    room = torch.empty(mt.mtgr_linear_i8_workspace_bytes(40, 72, 272), dtype=torch.uint8, device="cuda")
+    for n, buf in ((40, room), (9, None)):  # few rows: no workspace
+        out.zero_()
+        mt.mtgr_linear_i8(x[:n], w, ws, None, mt.MTGR_EPI_SILU, None, 0, out[:n], buf, status)
+        assert torch.equal(out[:n], ref[:n]) and (out[n:] == 0).all()
+    assert status.item() == 0
+    g, o, norm = torch.randn(1003, device="cuda"), torch.empty(1003, device="cuda"), torch.empty(1, device="cuda")
+    table = (L.MtgrGradTensor * 1)(L.MtgrGradTensor(g.data_ptr(), o.data_ptr(), 1003, mt.MTGR_F32, mt.MTGR_F32))
+    room = torch.zeros(mt.mtgr_grad_clip_workspace_bytes(table, 1), dtype=torch.uint8, device="cuda")
+    mt.mtgr_grad_clip(table, 1, 0.5, 0.25, norm, room, status)
+    plan = mt.GradientSet([g], [torch.empty_like(g)])
+    assert torch.equal(norm, plan.clip(0.5, 0.25)) and torch.equal(o, plan.outs[0]) and status.item() == 0

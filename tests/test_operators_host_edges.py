@@ -3,10 +3,12 @@
 import os
 import shutil
 import subprocess
+import types
 
 import pytest
 import torch
 
+import generative_recommendation_ranking_b200 as mt
 from generative_recommendation_ranking_b200 import ops
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -56,3 +58,14 @@ def test_a_given_workspace_is_checked():
     assert ops._given_ws(whole, 1024, -1) == 1024 and ops._given_ws(whole, 1025, -1) == 0
     assert ops._given_ws(whole[512:], 100, -1) == 512 and ops._given_ws(torch.zeros(8, 8), 100, -1) == 256
     assert ops._given_ws(whole[:0], 0, -1) == 0
+
+
+def test_wrappers_without_a_workspace():
+    # NULL is a workspace of no bytes: what needs none goes through, what needs one is refused
+    x = torch.zeros(0, 64)
+    w, ws = torch.zeros(8, 64, dtype=torch.int8), torch.zeros(8)
+    try:
+        mt.mtgr_linear_i8(x, w, ws, None, 0, None, 0, torch.zeros(0, 8), None, None,
+                          types.SimpleNamespace(cuda_stream=None))  # no rows: nothing is launched
+    except mt.MTGRError as e:
+        assert e.status == mt._lib.MTGR_ERR_UNSUPPORTED  # no GPU here
