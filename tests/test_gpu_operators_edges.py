@@ -270,3 +270,56 @@ def test_the_entry_points_one_by_one():
     mt.mtgr_grad_clip(table, 1, 0.5, 0.25, norm, room, status)
     plan = mt.GradientSet([g], [torch.empty_like(g)])
     assert torch.equal(norm, plan.clip(0.5, 0.25)) and torch.equal(o, plan.outs[0]) and status.item() == 0
+
+
+# --------------------------------------------- long runs of the backward --
+def check_long(T, d, order, rows, G=4, gate="linear", branch=torch.bfloat16):
+    """The backward over many rows a team against the oracle, chunk by chunk of rows.
+
+    A team's gradient sums are fp32 over its run of at most `rows` rows: as many
+    roundings of partial sums, each at most 2^-24 of the terms' magnitudes added up,
+    beside the 128 of a term; the teams are added up in fp64."""
+    rng = np.random.default_rng(T + d)
+    gid = rng.integers(0, G, T)
+    if order == "sorted":
+        gid = np.sort(gid)
+    elif order == "users":  # runs of every group, some shorter than a team's rows, some longer
+        gid = np.repeat(np.arange(T) % G, rng.integers(1, 60, T))[:T]
+    dev, r = case(T, d, branch, gate=gate, G=G, gid=gid)
+    dh, dy = upstream(T, d)
+    out = mt.boundary_backward(**dev, dh=dh, dy=dy, gate=gate)
+    names = ("post_gamma", "post_beta", "scale", "pre_gamma", "pre_beta")
+    want, mag = ({n: np.zeros((G, d)) for n in names} for _ in range(2))
+    step = max(1, 4_000_000 // d)
+    for t in range(0, T, step):
+        cut = slice(t, min(T, t + step))
+        part = {k: (v[cut] if k in ("x", "o", "u", "gid") and v is not None else v) for k, v in r.items()}
+        a, b = host(dh[cut]), host(dy[cut])
+        w = op.boundary_backward(**oracle_args(part), dh=a, dy=b, kind=gate)
+        m = mags(part, gate, a, b)
+        for k in w:
+            if k in names:
+                want[k] += w[k]
+                mag[k] += m[k]
+            else:
+                near(out[k][cut], w[k], m[k], f"{k}, rows from {t}")
+    for n in names:
+        g = host(out[n])
+        tol = (128 + rows) * 2.0 ** -24 * mag[n] + 2.0 ** -24 * np.abs(want[n])
+        assert (np.abs(g - want[n]) <= tol).all(), (n, np.abs(g - want[n]).max())
+
+
+# 17 rows a team on 148 SMs, the last team's fewer
+LONG = [(120011, 64), (60013, 128), (30011, 256), (20011, 512), (10007, 1024), (5003, 2048), (2503, 4096), (2503, 8192)]
+
+
+@pytest.mark.parametrize("T,d", LONG)
+@pytest.mark.parametrize("order", ["sorted", "users", "any"])
+def test_boundary_backward_long_runs(T, d, order):
+    check_long(T, d, order, 32)
+
+
+# 113, 113 and 50 rows a team
+@pytest.mark.parametrize("T,d,G,gate,rows", [(200003, 256, 4, "silu", 128), (400009, 120, 4, "none", 128), (2503, 8192, 32, "linear", 64)])
+def test_boundary_backward_a_hundred_rows_a_team(T, d, G, gate, rows):
+    check_long(T, d, "users", rows, G, gate, torch.float16)
