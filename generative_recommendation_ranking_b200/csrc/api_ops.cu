@@ -43,6 +43,9 @@ int boundary_check(const mtgr_boundary_params* p, int32_t T, int32_t o_dtype, in
   return MTGR_OK;
 }
 
+// An output that is an operand of its own product: blocks would write what others still read.
+bool is_operand(const void* out, const void* a, const void* b) { return out != nullptr && (out == a || out == b); }
+
 // Arguments of the int8 product that do not depend on how a is given.
 int gemm_i8_check(int32_t M, int32_t N, int32_t K, const void* b, const float* sb, const float* bias,
                   int32_t epi, const float* resid, int32_t q_cols, int32_t out_dtype, const void* out) {
@@ -158,7 +161,7 @@ MTGR_API int mtgr_quantize_rows(int32_t M, int32_t K, int32_t x_dtype, const voi
   const int rc = quant_check(M, K, x_dtype, d_x, ld_x);
   if (rc != MTGR_OK) return rc;
   if (M > 0 && (d_q == nullptr || d_scale == nullptr)) return MTGR_ERR_INVALID_ARG;
-  if (!aligned16(d_q)) return MTGR_ERR_INVALID_ARG;
+  if (!aligned16(d_q) || is_operand(d_q, d_x, nullptr)) return MTGR_ERR_INVALID_ARG;
   TimedScope tsc(MTGR_TIMER_ROWS, as_stream(stream), M > 0 ? 1 : 0);
   return launch_quantize_rows(M, K, x_dtype, d_x, ld_x, d_q, d_scale, as_stream(stream));
 }
@@ -170,6 +173,7 @@ MTGR_API int mtgr_gemm_i8(int32_t M, int32_t N, int32_t K, const int8_t* d_a, co
   const int rc = gemm_i8_check(M, N, K, d_b, d_b_scale, d_bias, epi, d_resid, q_cols, out_dtype, d_out);
   if (rc != MTGR_OK) return rc;
   if ((M > 0 && N > 0 && (d_a == nullptr || d_a_scale == nullptr)) || !aligned16(d_a)) return MTGR_ERR_INVALID_ARG;
+  if (is_operand(d_out, d_a, d_b)) return MTGR_ERR_INVALID_ARG;
   if (!device_is_sm100()) return MTGR_ERR_UNSUPPORTED;
   TimedScope tsc(MTGR_TIMER_GEMM_QKVU, as_stream(stream), M > 0 && N > 0 ? 1 : 0);
   if (gemm_i8_is_few(M, N, K))
@@ -195,6 +199,7 @@ MTGR_API int mtgr_linear_i8(int32_t M, int32_t N, int32_t K, int32_t x_dtype, co
   const size_t need = mtgr_linear_i8_workspace_bytes(M, N, K);
   if (ws_bytes < need) return MTGR_ERR_CAPACITY;
   if ((need > 0 && d_ws == nullptr) || !aligned16(d_ws)) return MTGR_ERR_INVALID_ARG;
+  if (is_operand(d_out, d_x, d_w)) return MTGR_ERR_INVALID_ARG;
   if (!device_is_sm100()) return MTGR_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return MTGR_OK;
   if (need == 0) {

@@ -69,3 +69,14 @@ def test_wrappers_without_a_workspace():
                           types.SimpleNamespace(cuda_stream=None))  # no rows: nothing is launched
     except mt.MTGRError as e:
         assert e.status == mt._lib.MTGR_ERR_UNSUPPORTED  # no GPU here
+
+
+def test_an_output_that_is_an_operand_is_refused():
+    # other blocks still read what a block would write; addresses are never read here
+    lib, (a, b, c, d) = mt.load(), (0x100000, 0x200000, 0x300000, 0x400000)
+    invalid, f32 = mt._lib.MTGR_ERR_INVALID_ARG, mt.MTGR_F32
+    for out in (a, b):
+        assert lib.mtgr_gemm_i8(40, 64, 64, a, c, b, c, None, 0, None, 0, f32, out, None, None) == invalid
+        for M in (9, 40):
+            assert lib.mtgr_linear_i8(M, 64, 64, f32, a, 64, b, c, None, 0, None, 0, f32, out, d, 1 << 20, None, None) == invalid
+    assert lib.mtgr_quantize_rows(40, 64, f32, a, 64, a, c, None) == invalid
