@@ -9,7 +9,7 @@ import torch
 
 import generative_recommendation_ranking_b200 as mt
 from oracle import operators as op
-from test_gpu_operators import EPIS, case, host, mags, near, oracle_args, product_case, upstream
+from test_gpu_operators import EPIS, NAMES, case, host, mags, near, oracle_args, product_case, upstream
 
 pytestmark = pytest.mark.gpu
 
@@ -237,7 +237,7 @@ def test_the_entry_points_one_by_one():
     # the binding's wrappers of the library's entry points, on the caller's buffers
     L = mt._lib
     dev, _ = case(40, 264, gate="silu")
-    names = ("post_gamma", "post_beta", "scale", "pre_gamma", "pre_beta")
+    names = NAMES
     p = L.MtgrBoundaryParams(264, 4, 1e-5, L.MTGR_GATE_SILU, *[dev[n].data_ptr() for n in names])
     h, y, ys = torch.empty(40, 264, device="cuda"), torch.empty(40, 264, dtype=torch.int8, device="cuda"), torch.empty(40, device="cuda")
     mt.mtgr_boundary_fwd(p, 40, dev["group_id"], dev["o"], dev["u"], dev["x"], h, y, ys)
@@ -288,7 +288,7 @@ def check_long(T, d, order, rows, G=4, gate="linear", branch=torch.bfloat16):
     dev, r = case(T, d, branch, gate=gate, G=G, gid=gid)
     dh, dy = upstream(T, d)
     out = mt.boundary_backward(**dev, dh=dh, dy=dy, gate=gate)
-    names = ("post_gamma", "post_beta", "scale", "pre_gamma", "pre_beta")
+    names = NAMES
     want, mag = ({n: np.zeros((G, d)) for n in names} for _ in range(2))
     step = max(1, 4_000_000 // d)
     for t in range(0, T, step):
@@ -323,3 +323,112 @@ def test_boundary_backward_long_runs(T, d, order):
 @pytest.mark.parametrize("T,d,G,gate,rows", [(200003, 256, 4, "silu", 128), (400009, 120, 4, "none", 128), (2503, 8192, 32, "linear", 64)])
 def test_boundary_backward_a_hundred_rows_a_team(T, d, G, gate, rows):
     check_long(T, d, "users", rows, G, gate, torch.float16)
+
+
+# ------------------------------------ in place, past 32 bits, in a capture --
+@pytest.mark.parametrize("d", [8, 64, 104, 256, 512, 1024, 8192])
+@pytest.mark.parametrize("stream", [torch.float32, torch.bfloat16])
+def test_boundary_backward_dx_in_place_of_dh(d, stream):
+    T = 1003 if d < 8192 else 301
+    dev, _ = case(T, d, stream=stream)
+    dh, dy = upstream(T, d, stream)
+    want = mt.boundary_backward(**dev, dh=dh, dy=dy)
+    p = mt._lib.MtgrBoundaryParams(d, 4, 1e-5, mt._lib.MTGR_GATE_LINEAR, *[dev[n].data_ptr() for n in NAMES])
+    par = {n: torch.empty(4, d, device="cuda") for n in NAMES}
+    do, du = torch.empty_like(want["do"]), torch.empty_like(want["du"])
+    ws = torch.empty(mt._lib.mtgr_boundary_bwd_workspace_bytes(T, p), dtype=torch.uint8, device="cuda")
+    mt._lib.mtgr_boundary_bwd(p, T, dev["group_id"], dev["o"], dev["u"], dev["x"], dh, dy, do, du, dh,
+                        mt._lib.MtgrBoundaryGrads(*[par[n].data_ptr() for n in NAMES]), ws)
+    assert torch.equal(dh, want["dx"]) and torch.equal(do, want["do"]) and torch.equal(du, want["du"])
+    assert all(torch.equal(par[n], want[n]) for n in NAMES)
+
+
+def test_boundary_past_32_bits():
+    # 2^31 + values: the last rows against a call on them alone
+    T, d = 4_200_000, 512
+    g = torch.Generator(device="cuda").manual_seed(0)
+    r = lambda *s, t: torch.empty(*s, device="cuda", dtype=t).normal_(generator=g)  # noqa: E731
+    dev = dict(x=r(T, d, t=torch.float32), o=r(T, d, t=torch.bfloat16), u=r(T, d, t=torch.bfloat16),
+               group_id=torch.randint(0, 4, (T,), generator=g, device="cuda", dtype=torch.int8),
+               **{n: r(4, d, t=torch.float32) for n in NAMES})
+    n = 777
+    last = {k: (v[-n:] if v.shape[0] == T else v) for k, v in dev.items()}
+    got = mt.boundary_forward(**dev, y_dtype=torch.int8)
+    want = mt.boundary_forward(**last, y_dtype=torch.int8)
+    assert all(torch.equal(a[-n:], b) for a, b in zip(got, want))
+    del got, want
+    dh, dy = r(T, d, t=torch.float32), r(T, d, t=torch.bfloat16)
+    got = mt.boundary_backward(**dev, dh=dh, dy=dy)
+    want = mt.boundary_backward(**last, dh=dh[-n:], dy=dy[-n:])
+    assert all(torch.equal(got[k][-n:], want[k]) for k in ("dx", "do", "du"))
+    # dbeta of the norm before: dy's sums, at most 3552 rows a team in fp32
+    pre = torch.stack([dy[dev["group_id"] == g].double().sum(0) for g in range(4)])
+    mag = torch.stack([dy[dev["group_id"] == g].double().abs().sum(0) for g in range(4)])
+    assert ((got["pre_beta"] - pre).abs() <= (4000 * 2.0 ** -24) * mag).all()
+
+
+def test_quantise_and_product_past_32_bits():
+    M, K, N = 4_200_000, 512, 520
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.empty(M, K, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    w, ws = mt.quantize_rows(torch.randn(N, K, device="cuda"))
+    q, s = mt.quantize_rows(x)
+    n = 777
+    ql, sl = mt.quantize_rows(x[-n:])
+    assert torch.equal(q[-n:], ql) and torch.equal(s[-n:], sl)
+    for out, epi in ((torch.float32, "resid"), (torch.float16, "none")):
+        resid = torch.empty(M, N, device="cuda").normal_(generator=g) if epi == "resid" else None
+        got = mt.gemm_i8(q, s, w, ws, None, EPIS[epi], resid, 0, out)
+        want = mt.gemm_i8(ql, sl, w, ws, None, EPIS[epi], None if resid is None else resid[-n:], 0, out)
+        assert torch.equal(got[-n:], want)
+        if resid is None:
+            assert torch.equal(mt.linear_i8(x, w, ws, out_dtype=out), got)
+    wide = x.view(-1)[:4 * 512 * (M // 4)].view(M // 4, 4 * 512)[:, -512:]
+    assert torch.equal(mt.linear_i8(wide, w, ws)[-n:], mt.linear_i8(wide[-n:].contiguous(), w, ws))
+
+
+def test_wide_weights_past_32_bits():
+    # N K past 2^31
+    N, K = 70_000 * 8, 4096
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    ws = torch.ones(N, device="cuda") * 1e-5
+    for M in (5, 40):
+        q = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+        s = torch.ones(M, device="cuda")
+        got = mt.gemm_i8(q, s, w, ws)
+        assert torch.equal(got[:, -800:], mt.gemm_i8(q, s, w[-800:], ws[-800:]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_clip_past_32_bits(dtype):
+    n = (1 << 31) + 12345
+    g = torch.zeros(n, device="cuda", dtype=dtype)
+    g[-5000:] = 3.0
+    g[:3] = 4.0
+    s = mt.GradientSet([g, torch.ones(7, device="cuda")])
+    want = (9.0 * 5000 + 16 * 3 + 7) ** 0.5
+    assert abs(s.clip(1.0).item() - want) <= 1e-6 * want
+    f = 1.0 / (want + 1e-6)
+    assert torch.allclose(g[-5000:].float(), torch.full((5000,), 3 * f, device="cuda"), rtol=1.01 * 2.0 ** -8)
+    assert torch.allclose(g[:3].float(), torch.full((3,), 4 * f, device="cuda"), rtol=1.01 * 2.0 ** -8)
+    assert (g[3:-5000] == 0).all()
+
+
+def test_set_made_in_a_capture():
+    grads = [torch.randn(100003, device="cuda"), torch.randn(77, device="cuda")]
+    want = mt.GradientSet(grads, [torch.empty_like(x) for x in grads])
+    norm = want.clip(0.5)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    outs = [torch.empty_like(x) for x in grads]
+    with torch.cuda.graph(graph):
+        s = mt.GradientSet(grads, outs)
+        n = s.clip(0.5)
+    for _ in range(3):
+        [o.zero_() for o in outs]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(n, norm) and all(torch.equal(a, b) for a, b in zip(outs, want.outs))
+        s.check()
+    assert torch.equal(s.clip(0.5), norm)
