@@ -221,8 +221,6 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if type(stream) is int:  # a cudaStream_t
-        return stream
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream

@@ -22,8 +22,7 @@ template <typename T, int THREADS, int VPL>
 __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
     quantize_rows_kernel(int32_t M, int32_t K, const T* x, int64_t ld_x, int8_t* q, float* scale) {
   constexpr bool BLOCK = THREADS != 32;
-  __shared__ float part[BLOCK ? 2 : 1][1][32];
-  Team<1, BLOCK> team(part);
+  __shared__ uint32_t part[BLOCK ? 32 : 1];
   dependents_may_launch();
   const int tl = threadIdx.x % THREADS;
   const int64_t m = BLOCK ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -39,7 +38,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
 #pragma unroll
   for (int k = 0; k < VPL; ++k)
     if (tl + THREADS * k < nv) mx = max_nan(mx, max_abs8(r[k]));
-  const RowScale rs = row_scale(team.max_bits(__float_as_uint(mx)));
+  const RowScale rs = row_scale(team_max_bits<BLOCK>(__float_as_uint(mx), part));
   if (tl == 0) scale[m] = rs.s;
 #pragma unroll
   for (int k = 0; k < VPL; ++k) {

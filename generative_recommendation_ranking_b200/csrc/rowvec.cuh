@@ -1,6 +1,6 @@
 // Row vectors of eight elements for the row kernels (one row of [rows][d] per
-// team of threads): 16- or 32-byte loads and stores of fp32, bf16 and f16, sums
-// and maxima over a team, and the quantisation of a row to signed bytes.
+// team of threads): 16- or 32-byte loads and stores of fp32, bf16 and f16, maxima over
+// a team, and the quantisation of a row to signed bytes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -23,7 +23,6 @@ struct Vec8<float> {
     a = *reinterpret_cast<const float4*>(p);
     b = *(reinterpret_cast<const float4*>(p) + 1);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const;
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -35,7 +34,6 @@ template <>
 struct Vec8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const;
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -51,7 +49,6 @@ template <>
 struct Vec8<__half> {
   uint4 a;
   __device__ __forceinline__ void load(const __half* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void pairs(uint64_t (&v)[4]) const;
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
@@ -63,12 +60,6 @@ struct Vec8<__half> {
     }
   }
 };
-
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  Vec8<float> r;
-  r.load(p);
-  r.unpack(v);
-}
 
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -172,75 +163,20 @@ __device__ __forceinline__ void store_pairs(T* p, const f2 (&v)[4]) {
 }
 
 // ------------------------------------------------------------------ teams --
-// A row's threads: one warp (TEAM = 32), or a whole block (TEAM = blockDim.x,
-// a multiple of 32 up to 1024), whose warps meet in shared memory. Every
-// thread of the team gets the result, the same bits in each.
-template <int N, bool BLOCK>
-struct Team {
-  // one slot of partials per reduction in flight: two, used in turn, so that
-  // one barrier per reduction is enough
-  float (*part)[N][32];
-  int turn = 0;
-
-  __device__ __forceinline__ explicit Team(float (*p)[N][32]) : part(p) {}
-
-  __device__ __forceinline__ void sum(float (&v)[N]) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if constexpr (BLOCK) {
-      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-      if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) part[turn][i][warp] = v[i];
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float s = lane < nw ? part[turn][i][lane] : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        v[i] = s;
-      }
-      turn ^= 1;
-    }
+// Maximum of non-negative values by their bits over a row's threads: one warp, or a
+// whole block, whose warps meet in shared memory (part: 32 words). A NaN is above every
+// number and an infinity, so it is not lost. Every thread gets the result.
+template <bool BLOCK>
+__device__ __forceinline__ uint32_t team_max_bits(uint32_t a, uint32_t* part) {
+  a = __reduce_max_sync(0xffffffffu, a);
+  if constexpr (BLOCK) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    if (lane == 0) part[warp] = a;
+    __syncthreads();
+    a = __reduce_max_sync(0xffffffffu, lane < nw ? part[lane] : 0u);
   }
-  __device__ __forceinline__ float sum1(float a) {
-    float v[N] = {};
-    v[0] = a;
-    if constexpr (N == 1) {
-      sum(v);
-      return v[0];
-    } else {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-      if constexpr (BLOCK) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-        if (lane == 0) part[turn][0][warp] = a;
-        __syncthreads();
-        a = lane < nw ? part[turn][0][lane] : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-        turn ^= 1;
-      }
-      return a;
-    }
-  }
-  // maximum of non-negative values by their bits: a NaN is above every number
-  // and an infinity, so it is not lost
-  __device__ __forceinline__ uint32_t max_bits(uint32_t a) {
-    a = __reduce_max_sync(0xffffffffu, a);
-    if constexpr (BLOCK) {
-      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-      if (lane == 0) part[turn][0][warp] = __uint_as_float(a);
-      __syncthreads();
-      a = lane < nw ? __float_as_uint(part[turn][0][lane]) : 0u;
-      a = __reduce_max_sync(0xffffffffu, a);
-      turn ^= 1;
-    }
-    return a;
-  }
-};
+  return a;
+}
 
 // -------------------------------------------------- rows in signed 8 bits --
 // A row's scale s = max(max |v|, 2^-100) * (1 / 127), 1 / 127 rounded to fp32, and
