@@ -1,9 +1,16 @@
 """User-facing API over libmtgr.so: device buffers (through PyTorch) plus calls
 into the C ABI. Every step of the forward runs in the library's CUDA kernels;
 this module only sizes and allocates buffers and marshals arguments.
+
+With ``stream`` a call works on that stream and allocates its memory; the order
+with other streams is the caller's: inputs ready for ``stream`` before the call,
+results read behind it.
 """
 
 from __future__ import annotations
+
+import functools
+import inspect
 
 import numpy as np
 import torch
@@ -12,6 +19,43 @@ from . import _lib
 from ._lib import (MTGR_BF16, MTGR_F16, MTGR_F32, MtgrBatch, MtgrBlockParams, TILE_M, TILE_N)
 
 EPS = 1e-5
+
+
+def _record(v, stream) -> None:
+    """Keeps the memory of every tensor in ``v`` until ``stream`` has got past its release."""
+    if isinstance(v, torch.Tensor):
+        if v.is_cuda:
+            v.record_stream(stream)
+    elif isinstance(v, (tuple, list)):
+        for t in v:
+            _record(t, stream)
+    elif isinstance(v, dict):
+        _record(list(v.values()), stream)
+    elif isinstance(v, (PackedBatch, ContextCache, BatchContextCache)):
+        _record(vars(v), stream)
+
+
+def _on_its_stream(fn):
+    """Runs ``fn`` with its argument ``stream`` as the current one: what it allocates,
+    copies or zeroes is ordered on the stream that its kernels run on, and a buffer that
+    it drops is not handed out elsewhere while they run. Its results are kept for the
+    stream it was called on, where their reader is."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return fn(*args, **kwargs)
+        now = torch.cuda.current_stream(stream.device)
+        if now == stream:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kwargs)
+        _record(args[0] if fn.__name__ == "__init__" else out, now)
+        return out
+
+    return call
 
 
 def capacities(lens: np.ndarray) -> tuple:
@@ -41,6 +85,7 @@ class PackedBatch:
     ``stream``.
     """
 
+    @_on_its_stream
     def __init__(self, lens, ts, device="cuda", norm=None, stream=None):
         lens = np.ascontiguousarray(np.asarray(lens, dtype=np.int32).reshape(-1, 4))
         self.lens = lens
@@ -162,6 +207,7 @@ def _ws(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+@_on_its_stream
 def hstu_block_forward(w: BlockWeights, batch: PackedBatch, x: torch.Tensor, out=None, ws=None,
                        stream=None) -> torch.Tensor:
     """One HSTU block: x [T, d] float32 on the device -> new [T, d] float32."""
@@ -178,6 +224,7 @@ GRAD_NAMES = ("gln1_gamma", "gln1_beta", "w_qkvu", "b_qkvu", "gln2_gamma", "gln2
               "w2", "b2")
 
 
+@_on_its_stream
 def hstu_block_forward_train(w: BlockWeights, batch: PackedBatch, x: torch.Tensor, out=None,
                              saved=None, stream=None):
     """One HSTU block forward that keeps what its backward reads. Returns
@@ -191,6 +238,7 @@ def hstu_block_forward_train(w: BlockWeights, batch: PackedBatch, x: torch.Tenso
     return out, saved
 
 
+@_on_its_stream
 def hstu_block_backward(w: BlockWeights, batch: PackedBatch, x: torch.Tensor, saved: torch.Tensor,
                         dy: torch.Tensor, bias_grads: bool = True, ws=None, stream=None):
     """Gradients of one HSTU block for the upstream gradient dy [T, d]
@@ -217,6 +265,7 @@ def stack_workspace(layers, batch: PackedBatch) -> torch.Tensor:
     return _ws(_lib.mtgr_stack_workspace_bytes(batch.T, [l.c for l in layers]), batch.device)
 
 
+@_on_its_stream
 def hstu_stack_forward(layers, batch: PackedBatch, x: torch.Tensor, out=None, ws=None,
                        stream=None) -> torch.Tensor:
     """L stacked HSTU blocks sharing the batch's mask metadata."""
@@ -228,6 +277,7 @@ def hstu_stack_forward(layers, batch: PackedBatch, x: torch.Tensor, out=None, ws
     return out
 
 
+@_on_its_stream
 def group_layernorm_pooled(batch: PackedBatch, x: torch.Tensor, gamma: torch.Tensor,
                            beta: torch.Tensor, eps: float = EPS, out_dtype=None, stream=None):
     """GroupLN with one mean and variance per (user, group) segment."""
@@ -237,6 +287,7 @@ def group_layernorm_pooled(batch: PackedBatch, x: torch.Tensor, gamma: torch.Ten
     return y
 
 
+@_on_its_stream
 def hstu_attention(batch: PackedBatch, qkvu: torch.Tensor, d: int, H: int,
                    out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """G = (silu(Q K^T) (.) M / N) V (.) U for qkvu [T, 4d] (bf16, f16 or f32)."""
@@ -245,6 +296,7 @@ def hstu_attention(batch: PackedBatch, qkvu: torch.Tensor, d: int, H: int,
     return g
 
 
+@_on_its_stream
 def group_layernorm(x: torch.Tensor, group_id: torch.Tensor, gamma: torch.Tensor,
                     beta: torch.Tensor, eps: float = EPS, out_dtype=None, stream=None):
     T, d = x.shape
@@ -253,6 +305,7 @@ def group_layernorm(x: torch.Tensor, group_id: torch.Tensor, gamma: torch.Tensor
     return y
 
 
+@_on_its_stream
 def gemm(a: torch.Tensor, b: torch.Tensor, bias=None, epi: int = 0, resid=None, q_cols: int = 0,
          out_dtype=torch.float32, status=None, stream=None) -> torch.Tensor:
     """out = epi(a b^T + bias); a [M, K], b [N, K]."""
@@ -263,6 +316,7 @@ def gemm(a: torch.Tensor, b: torch.Tensor, bias=None, epi: int = 0, resid=None, 
     return out
 
 
+@_on_its_stream
 def gemm_wgrad(a: torch.Tensor, b: torch.Tensor, out=None, status=None, stream=None) -> torch.Tensor:
     """out [M, N] fp32 (+)= a^T b; a [T, M] and b [T, N] bf16, token-major.
     With ``out`` given the sums are added to it, else a zeroed one is made."""
@@ -293,6 +347,7 @@ class ContextCache:
     not read). ``out`` holds the stack's output on the context rows.
     """
 
+    @_on_its_stream
     def __init__(self, layers, n_u: int, n_s: int, n_r: int, ts_ctx, x_ctx: torch.Tensor,
                  k_total: int, max_chunk: int, stream=None):
         self.layers = list(layers)
@@ -320,6 +375,7 @@ class ContextCache:
         self.ctx_batch = batch
         self.ctx_ws = ws
 
+    @_on_its_stream
     def candidate_batch(self, ts_cand, stream=None) -> PackedBatch:
         """The virtual batch of one chunk: the context followed by the
         chunk's candidates, with the work list cut to the candidate rows."""
@@ -337,6 +393,7 @@ class ContextCache:
         return _ws(_lib.mtgr_stack_rows_workspace_bytes(self.n_ctx + k, self.n_ctx, self.c_layers),
                    self.cache.device)
 
+    @_on_its_stream
     def score(self, ts_cand, x_cand: torch.Tensor, out=None, ws=None, batch=None,
               stream=None) -> torch.Tensor:
         """Stack output [k, d] float32 of k candidates (features ``x_cand``
@@ -369,6 +426,7 @@ class BatchContextCache:
     the stack's output on all rows of this context pass.
     """
 
+    @_on_its_stream
     def __init__(self, layers, lens, ts, x: torch.Tensor, norm=None, stream=None):
         self.layers = list(layers)
         self.c_layers = [l.c for l in self.layers]
@@ -386,6 +444,7 @@ class BatchContextCache:
                                  stream)
         self.ctx_ws = ws  # kept for re-running the context pass in place
 
+    @_on_its_stream
     def candidate_batch(self, ts, stream=None) -> PackedBatch:
         """The batch of one candidate request: the same lens, with the packed
         timestamps ``ts`` holding the candidates' exposure times."""
@@ -395,6 +454,7 @@ class BatchContextCache:
         return _ws(_lib.mtgr_stack_candidates_workspace_bytes(self.batch.B, self.T, self.k_total,
                                                               self.c_layers), self.cache.device)
 
+    @_on_its_stream
     def score(self, ts, x_cand: torch.Tensor, out=None, ws=None, batch=None,
               stream=None) -> torch.Tensor:
         """Stack output [K_total, d] float32 of the candidates (features
@@ -436,6 +496,7 @@ class TokenMLPs:
         self.d = self.t["s"][2].shape[0]
 
 
+@_on_its_stream
 def tokenize(mlps: TokenMLPs, batch: PackedBatch, e: list, out=None, ws=None,
              stream=None) -> torch.Tensor:
     """Block input X [T, d] float32 from the per-domain inputs ``e`` = [E_U,
@@ -475,6 +536,7 @@ class CandidateHeads:
         self.n_tasks = n_tasks
 
 
+@_on_its_stream
 def candidate_heads(heads: CandidateHeads, batch: PackedBatch, x: torch.Tensor, out=None, ws=None,
                     stream=None) -> torch.Tensor:
     """Logits [K_total, n_tasks] float32 of the batch's candidates (user by
