@@ -16,8 +16,8 @@
 //           the 256 columns of b): many rows.
 //   CG = 1: one CTA, 128 x 64 tiles, so that a few hundred rows spread over the SMs;
 //           with a long k and too few of them, a cluster of CTAs for each (below).
-//   KEEP_B (pairs, k <= 512): a pair stays in its 256 columns and keeps their b in
-//           shared memory, which halves what L2 hands to the SMs.
+//   KEEP_B (pairs, k <= 512, where it gains: keeps_b): a pair stays in its 256 columns and
+//           keeps their b in shared memory, which halves what L2 hands to the SMs.
 // Measured on one B200, bursts of 20: 8192^3 at 2.9-3.1 P op/s, where the operands'
 // way out of L2 (about 12 TB/s) bounds it (without b's loads 3.7); 131075 x 2048 x 512
 // to f16 146 us (b reloaded: 152), its output's way to DRAM beside the epilogue (no
@@ -457,6 +457,21 @@ __global__ void __launch_bounds__(Epi<OUT, CG, KEEP_B>::kThreads, 1)
 
 constexpr int kMaxDevices = 64;
 
+// Whether pairs keep b in shared memory (k <= kKeepK), on `units` pairs. A pair stays in one
+// column of tiles, so units % n_tiles of them have no work; that has to be little. Where
+// rows of k bytes are not whole 128-byte lines, loading b again costs most: kept against
+// reloaded 100003 x 2048 x 272 to f16 99 / 114 us, x 448 109 / 118, x 496 125 / 143; up to
+// ten of 74 pairs idle it stays ahead (100003 x 4096 x 448 236 / 245), at 14 no more (x 3840:
+// 236 / 225). With whole lines it gains at k = 512 alone, with two pairs idle (131075 x 2048 x
+// 512 140 / 145, x 2560 with four 189 / 186) and four row tiles a pair (10000 x 1024 x 512,
+// two of them: 14.4 / 12.7), and not below (131075 x 2048 x 384 146 / 136, x 256 136 / 125).
+inline bool keeps_b(int units, int64_t m_tiles, int n_tiles, int K) {
+  if (units < n_tiles) return false;
+  const int idle = units % n_tiles;
+  if (K % BK != 0) return 7 * idle <= units;
+  return K == kKeepK && 32 * idle <= units && m_tiles >= 4 * (units / n_tiles);
+}
+
 template <int EPI, int OUT, int CG, bool KEEP_B>
 int launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const Args& args,
              cudaStream_t s, bool dependent) {
@@ -492,9 +507,9 @@ int launch_t(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to
     }
     resident[dev].store(units, std::memory_order_relaxed);
   }
-  const int64_t tiles = (((int64_t)args.M + BM * CG - 1) / (BM * CG)) *
-                        ((args.N + Shape<CG>::kBN - 1) / Shape<CG>::kBN);
-  if (KEEP_B && units < (args.N + Shape<CG>::kBN - 1) / Shape<CG>::kBN)  // a pair per column at least
+  const int n_tiles = (args.N + Shape<CG>::kBN - 1) / Shape<CG>::kBN;
+  const int64_t m_tiles = ((int64_t)args.M + BM * CG - 1) / (BM * CG), tiles = m_tiles * n_tiles;
+  if (KEEP_B && !keeps_b(units, m_tiles, n_tiles, args.K))
     return launch_t<EPI, OUT, CG, false>(ta, tb, to, args, s, dependent);
   if (tiles > 0x3fffffff) return MTGR_ERR_UNSUPPORTED;  // the kernel counts tiles in 32 bits
   cfg.gridDim = dim3((unsigned)(CG * (tiles < units ? tiles : units)));
@@ -520,7 +535,7 @@ int launch_cg(int M, int N, int K, const int8_t* a, const int8_t* b, int epi, in
            : make_tmap_2d(&to, out, CU_TENSOR_MAP_DATA_TYPE_UINT16, (uint64_t)N, (uint64_t)M,
                           (uint64_t)N * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc != MTGR_OK) return rc;
-  // b's tile stays where k is short and every pair has several row tiles
+  // b's tile may stay where k is short and every column of tiles has four pairs or more
   const bool keep = CG == 2 && K <= kKeepK && (N + S::kBN - 1) / S::kBN <= device_sm_count() / 8;
 #define MTGR_FORM(E, O) \
   if (epi == E && out_dtype == O)                                                     \

@@ -432,3 +432,24 @@ def test_set_made_in_a_capture():
         assert torch.equal(n, norm) and all(torch.equal(a, b) for a, b in zip(outs, want.outs))
         s.check()
     assert torch.equal(s.clip(0.5), norm)
+
+
+@pytest.mark.parametrize("M,N,K", [(10007, 2048, 512), (9001, 2048, 512), (20011, 1000, 512), (40003, 264, 512), (20011, 2560, 512), (10007, 2048, 384),
+                                   (5003, 1000, 496), (9001, 4096, 272), (9001, 3840, 272), (40003, 72, 48), (10007, 4608, 512), (10007, 4616, 400)])
+@pytest.mark.parametrize("epi,out", [("none", torch.float16), ("silu", torch.float32), ("resid", torch.float32)])
+def test_weights_that_stay_in_shared_memory(M, N, K, epi, out):
+    # on either side of the rule for the pairs' columns: the same bits as 1000 rows, in small tiles
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    a, b = (torch.randint(-127, 128, (n, K), generator=g, device="cuda", dtype=torch.int8) for n in (M, N))
+    sa, sb = ((torch.rand(n, generator=g, device="cuda") + 0.5) / (73 * K ** 0.25) for n in (M, N))
+    bias, resid = (torch.randn(s, generator=g, device="cuda") for s in ((N,), (M, N)))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def product(rows):
+        return mt.gemm_i8(a[rows], sa[rows], b, sb, bias, EPIS[epi], resid[rows] if epi == "resid" else None, 32, out, status=status)
+
+    got = product(slice(0, M))
+    for t in list(range(0, M, 1000)):
+        rows = slice(t, min(M, t + 1000))
+        assert torch.equal(got[rows], product(rows)), t
+    assert status.item() == 0
