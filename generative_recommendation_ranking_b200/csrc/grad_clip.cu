@@ -139,20 +139,36 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { re
 template <>
 __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
+// The factor of the clip, c 2^e; e = 0 where c is one of fp32's normal numbers. Below them
+// (an exploded step: norm 1e38 to 1) c would have lost bits, or be 0, while its products
+// with such gradients are ordinary numbers.
+struct Factor {
+  float c;
+  int32_t e;
+};
+__device__ __forceinline__ Factor clip_factor(double norm, float max_norm, float inv_scale) {
+  const double ratio = (double)max_norm / (norm + 1e-6);
+  Factor f{inv_scale * fminf(1.0f, (float)ratio), 0};
+  if (f.c < 1.17549435e-38f) f.c = (float)frexp((double)inv_scale * fmin(1.0, ratio), &f.e);
+  return f;
+}
+
 template <typename T, typename O>
-__device__ __forceinline__ void scale_chunk(const void* gv, void* ov, int64_t e0, int64_t e1, float c) {
+__device__ __forceinline__ void scale_chunk(const void* gv, void* ov, int64_t e0, int64_t e1, float c, int32_t exp2) {
   const T* g = static_cast<const T*>(gv);
   O* o = static_cast<O*>(ov);
   const uintptr_t ga = reinterpret_cast<uintptr_t>(g + e0), oa = reinterpret_cast<uintptr_t>(o + e0);
   int64_t head = min(e1, e0 + (int64_t)(((16 - (ga & 15)) & 15) / sizeof(T)));
-  // vectors only where both sides are aligned from the same element on
+  // vectors only where both sides are aligned from the same element on, and the factor is an
+  // ordinary one
   const bool vec = ((oa + (uintptr_t)(head - e0) * sizeof(O)) & 15) == 0;
-  if (!vec) head = e1;
+  if (!vec || exp2 != 0) head = e1;
   const int64_t nv = (e1 - head) / 8;
   const int64_t singles = (head - e0) + (e1 - head - 8 * nv);
   for (int64_t i = threadIdx.x; i < singles; i += blockDim.x) {
     const int64_t e = i < head - e0 ? e0 + i : head + 8 * nv + (i - (head - e0));
-    o[e] = from_float<O>(to_float(g[e]) * c);
+    const float v = to_float(g[e]) * c;
+    o[e] = from_float<O>(exp2 == 0 ? v : ldexpf(v, exp2));
   }
 #pragma unroll 4
   for (int64_t i = threadIdx.x; i < nv; i += blockDim.x) {
@@ -181,21 +197,20 @@ __global__ void __launch_bounds__(256) grad_scale_kernel(const __grid_constant__
     if (!finite) set_status(status, MTGR_ERR_RANGE);
   }
   if (scale == 0 || !finite) return;
-  const float ratio = (float)((double)max_norm / (norm + 1e-6));
-  const float c = inv_scale * fminf(1.0f, ratio);
+  const Factor f = clip_factor(norm, max_norm, inv_scale);
   const int chunks = t.chunk0[t.count];
   // last chunks first: they are the ones L2 still holds
   for (int k = chunks - 1 - (int)blockIdx.x; k >= 0; k -= gridDim.x) {
     const int i = find_tensor(t, k);
     const int64_t e0 = (int64_t)(k - t.chunk0[i]) * kChunk;
     const int64_t e1 = min(t.n[i], e0 + kChunk);
-    if (c == 1.0f && t.g[i] == t.out[i]) continue;  // nothing to change in place
+    if (f.c == 1.0f && f.e == 0 && t.g[i] == t.out[i]) continue;  // nothing to change in place
     switch (t.dtype[i]) {
-      case MTGR_F32 | MTGR_F32 << 4: scale_chunk<float, float>(t.g[i], t.out[i], e0, e1, c); break;
-      case MTGR_BF16 | MTGR_BF16 << 4: scale_chunk<__nv_bfloat16, __nv_bfloat16>(t.g[i], t.out[i], e0, e1, c); break;
-      case MTGR_F16 | MTGR_F16 << 4: scale_chunk<__half, __half>(t.g[i], t.out[i], e0, e1, c); break;
-      case MTGR_BF16 | MTGR_F32 << 4: scale_chunk<__nv_bfloat16, float>(t.g[i], t.out[i], e0, e1, c); break;
-      default: scale_chunk<__half, float>(t.g[i], t.out[i], e0, e1, c); break;
+      case MTGR_F32 | MTGR_F32 << 4: scale_chunk<float, float>(t.g[i], t.out[i], e0, e1, f.c, f.e); break;
+      case MTGR_BF16 | MTGR_BF16 << 4: scale_chunk<__nv_bfloat16, __nv_bfloat16>(t.g[i], t.out[i], e0, e1, f.c, f.e); break;
+      case MTGR_F16 | MTGR_F16 << 4: scale_chunk<__half, __half>(t.g[i], t.out[i], e0, e1, f.c, f.e); break;
+      case MTGR_BF16 | MTGR_F32 << 4: scale_chunk<__nv_bfloat16, float>(t.g[i], t.out[i], e0, e1, f.c, f.e); break;
+      default: scale_chunk<__half, float>(t.g[i], t.out[i], e0, e1, f.c, f.e); break;
     }
   }
 }
@@ -300,14 +315,18 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks)
     if (!finite) set_status(status, MTGR_ERR_RANGE);
   }
   if (scale == 0 || !finite) return;
-  const float f = inv_scale * fminf(1.0f, (float)((double)max_norm / (norm + 1e-6)));
+  const Factor f = clip_factor(norm, max_norm, inv_scale);
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int k = which[i];
-    if (k < 0 || (f == 1.0f && t.g[k] == t.out[k])) continue;
+    if (k < 0 || (f.c == 1.0f && f.e == 0 && t.g[k] == t.out[k])) continue;
     const int64_t at = (int64_t)(blockIdx.x + i * (int)gridDim.x - t.chunk0[k]) * kHeldChunk + 8 * threadIdx.x;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] *= f;
+    for (int e = 0; e < 8; ++e) v[i][e] *= f.c;
+    if (f.e != 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = ldexpf(v[i][e], f.e);
+    }
     const int out = t.dtype[k] >> 4;
     if (out == MTGR_F32) store_some<float>(t.out[k], at, t.n[k], v[i]);
     else if (out == MTGR_BF16) store_some<__nv_bfloat16>(t.out[k], at, t.n[k], v[i]);

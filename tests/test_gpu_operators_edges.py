@@ -9,7 +9,8 @@ import torch
 
 import generative_recommendation_ranking_b200 as mt
 from oracle import operators as op
-from test_gpu_operators import EPIS, NAMES, case, host, mags, near, oracle_args, product_case, upstream
+from test_gpu_operators import (EPIS, HALF, NAMES, case, clip_case, host, mags, near, oracle_args, product_case,
+                                upstream)
 
 pytestmark = pytest.mark.gpu
 
@@ -453,3 +454,25 @@ def test_weights_that_stay_in_shared_memory(M, N, K, epi, out):
         rows = slice(t, min(M, t + 1000))
         assert torch.equal(got[rows], product(rows)), t
     assert status.item() == 0
+
+
+# -------------------------------------------------------------------- clip --
+@pytest.mark.parametrize("sizes", [[5003, 17], [16384 * 700, 40000], [300] * 200])
+@pytest.mark.parametrize("dtype,to", [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32)])
+@pytest.mark.parametrize("scale,max_norm,inv", [(1e34, 1.0, 1.0), (1e34, 1e-3, 1.0), (1e34, 1e-20, 1.0), (1e34, 1e30, 1e-38), (1e30, 1e-18, 0.25),
+                                                (3e33, 1e-40, 1.0)])
+def test_clip_factors_below_the_normal_numbers(sizes, dtype, to, scale, max_norm, inv):
+    # max_norm / norm of an exploded step: the clipped values are ordinary numbers though the
+    # factor is not one of fp32's
+    grads = clip_case(sizes, (dtype,), scale=scale)
+    outs = None if dtype == to else [torch.empty_like(x, dtype=to) for x in grads]
+    before = [host(x) for x in grads]
+    plan = mt.GradientSet(grads, outs)
+    norm = plan.clip(max_norm, inv).item()
+    want, clipped = op.grad_clip(before, float(np.float32(max_norm)), float(np.float32(inv)))
+    assert abs(norm - want) <= 8 * 2.0 ** -24 * want
+    tiny = 2.0 ** -149  # results below the normal numbers: a step of the subnormal ones, bf16's 2^-133
+    for o, w in zip(plan.outs, clipped):
+        tol = 128 * 2.0 ** -24 * np.abs(w) + HALF[to] * np.abs(w) * 1.001 + (tiny if to == torch.float32 else 2.0 ** -133)
+        assert (np.abs(host(o) - w) <= tol).all(), (np.abs(host(o) - w) / np.maximum(np.abs(w), 1e-300)).max()
+    plan.check()
