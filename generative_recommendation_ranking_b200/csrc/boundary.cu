@@ -1,11 +1,11 @@
 // The boundary between two blocks in one pass over the rows: the branch output o
 // is normalised by group, gated by u, scaled and added to the residual stream x,
 // and the next block's GroupLN reads the sum (GroupLN: fun-rec 7.3.3, the GLN
-// formula, per token over d with the token's group's gamma and beta; the gate
-// and the residual: summary page, Method, the block update equations):
+// formula, per token over d with the token's group's gamma and beta):
 //   n = GLN(o; post);  h = x + scale_g (.) n (.) f(u);  y = GLN(h; pre)
 // with f none, u or silu(u), each norm and the scale optional, and y in fp32,
-// bf16 or signed bytes with a scale per row.
+// bf16 or signed bytes with a scale per row. Between this library's blocks, which gate
+// inside their second norm, f and the post norm are absent: h = x + o, y = GLN(h).
 //
 // Backward, given dh (from the stream) and dy, with a = dy (.) gamma_pre and
 // ohat, hhat the normalised rows, 1/sigma their rstd:
@@ -17,8 +17,10 @@
 // At bf16 branch, fp32 stream and bf16 y the forward moves 14 bytes an element, which
 // bounds it, and the backward 22; that one is bound by its instructions' latency from
 // d = 256 on, at two warps a scheduler (0.70 of the copy rate). Statistics, sums and gradients are
-// held in fp32 (the sums over rows in fp32 per run of rows, then in fp64); the
-// backward forms h again from x, o and u instead of reading a rounded one.
+// held in fp32; the backward forms h again from x, o and u instead of reading a rounded
+// one. A parameter's gradient adds up in fp32 over a team's run of rows (registers; 169
+// rows at 200003 x 512, about T / 50 with 32 groups of 8192 columns, whose slots are limited),
+// then in fp64 over the teams.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -33,6 +35,9 @@ namespace mtgr {
 
 namespace {
 
+// e^-u by __expf, within 2 + 1.2 |u| ulp: far below a rounding of a bf16 or f16 branch, a few
+// ulp of an fp32 one. The quotient by __fdividef, within 2 ulp, and 0 where 1 + e^-u is
+// beyond 2^126 (|silu| below 1e-36).
 __device__ __forceinline__ float sigmoid_f32(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
 
 // silu as u / (1 + e^-u): e^-u = inf gives -0, as the limit does
@@ -288,7 +293,7 @@ int launch_fwd_t(const BoundaryFwdArgs& a, cudaStream_t s) {
 enum { kPreGamma = 0, kPreBeta = 1, kScale = 2, kPostGamma = 3, kPostBeta = 4 };
 
 // A row's inputs wait in shared memory: each thread copies its own eight values of
-// every input up to two rows ahead (cp.async) and reads back only those, so no barrier
+// every input one row ahead (cp.async; kAhead) and reads back only those, so no barrier
 // is needed, and the registers hold the sums instead. Stage layout: per thread
 // o, u (16 or 32 bytes), x, dh, dy; a thread's 16-byte pieces lie THREADS * 16
 // bytes apart, so that a warp's accesses fall in different banks.

@@ -7,9 +7,10 @@
 // table in the kernel's parameters, so nothing is copied to the device ahead. Large
 // sets are bound by HBM, small ones by the launch and the meeting of the blocks.
 //
-// Sums: squares of eight values in fp32, over those in fp64; where the eight
-// leave fp32's range (values beyond 1e18 or all below 1e-18), they are squared in
-// fp64. Blocks write their sums to the workspace, and they are added in a
+// Sums: squares of eight values in fp32, over those in fp64 (eight positive terms are off by
+// eight roundings of 2^-24 at most, which the root halves; fp64 throughout would take
+// eight conversions for one); where the eight leave fp32's range (values beyond 1e18 or all
+// below 1e-18), they are squared in fp64. Blocks write their sums to the workspace, and they are added in a
 // fixed order: no atomics on values, the same norm in every run.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -351,7 +351,10 @@ class GradientSet:
     type or float32); None: in place. The tensors' memory is read at every
     call, so a step writes new gradients into the same buffers. The set's
     workspaces and status word are its own: clips of one set are ordered by
-    the caller, two sets may run at once.
+    the caller, two sets may run at once. A norm may run beside a clip of the same
+    set if the clip writes other buffers (in place it would read what the clip
+    writes). A set made while a graph is captured is zeroed by that graph: it
+    is not used before the graph has run.
     """
 
     def __init__(self, grads, outs=None):
@@ -387,7 +390,7 @@ class GradientSet:
         # the norm alone
         self.c_norm = (MtgrGradTensor * n)(*[MtgrGradTensor(c.g, None, c.n, c.dtype, c.dtype) for c in self.c])
         with torch.cuda.device(self.device):
-            # one for each of the two calls, so that a norm may run beside a clip
+            # one for each of the two calls
             size = _lib.mtgr_grad_clip_workspace_bytes(self.c, n)
             self.ws, self.ws_norm = (torch.zeros(size, dtype=torch.uint8, device=self.device) for _ in range(2))
             self.status = torch.zeros(1, dtype=torch.int32, device=self.device)

@@ -655,15 +655,19 @@ MTGR_API int mtgr_hstu_block_bwd(const mtgr_block_params* p, const mtgr_batch* b
                                  size_t ws_bytes, mtgr_stream_t stream);
 
 /*
- * The boundary between two blocks in one pass: the norm after a block, its gate,
- * the residual scale and the norm before the next block (GroupLN: fun-rec 7.3.3,
- * the GLN formula; gate and residual: summary page, Method, the block update
- * equations). For every row i with group g = g(i):
+ * The boundary between two blocks in one pass: the norm of a branch's output, its
+ * gate, the residual scale, the sum with the residual stream and the norm before
+ * the next block (GroupLN: fun-rec 7.3.3, the GLN formula). For every row i with
+ * group g = g(i):
  *   n = GroupLN(o_i; post_gamma_g, post_beta_g)      (n = o_i without the post norm)
  *   h = x_i + scale_g (.) n (.) f(u_i)               (scale 1 if NULL)
  *   y = GroupLN(h; pre_gamma_g, pre_beta_g)          (no y without the pre norm)
  * Statistics as in mtgr_group_layernorm (per token over d, biased variance),
  * in fp32; y is taken from h before h is rounded to its type.
+ * mtgr_hstu_block_fwd gates inside its second norm and adds its residual itself
+ * (summary page, Method, the block update equations), so between its parts the form
+ * without post norm, gate and scale serves: h = x + o, y = GroupLN(h). The others are
+ * for stacks whose branches are normalised and gated on their way into the stream.
  */
 #define MTGR_GATE_NONE 0    /* f = 1; u is not read */
 #define MTGR_GATE_LINEAR 1  /* f(u) = u */
@@ -688,8 +692,9 @@ typedef struct mtgr_boundary_params {
  *   d_x, d_h [T][d] of x_dtype (MTGR_F32, MTGR_BF16); d_h may be d_x
  *   d_y [T][d] of y_dtype: MTGR_F32, MTGR_BF16, or MTGR_I8 with d_y_scale [T], as
  *     mtgr_quantize_rows would leave the fp32 y
- * All pointers but d_group_id and d_y_scale 16-byte aligned. Timer class
- * MTGR_TIMER_GLN.
+ * But for d_h as d_x, no output overlaps an input or another output. SiLU's e^-u is
+ * within 2 + 1.2 |u| fp32 ulp. All pointers but d_group_id and d_y_scale 16-byte
+ * aligned. Timer class MTGR_TIMER_GLN.
  */
 MTGR_API int mtgr_boundary_fwd(const mtgr_boundary_params* p, int32_t T, const int8_t* d_group_id,
                                int32_t o_dtype, const void* d_o, int64_t ld_o, const void* d_u,
@@ -713,8 +718,10 @@ typedef struct mtgr_boundary_grads {
  * with a gate, du [T][ld_du] (o_dtype; values past d of a row are left as they
  * are), and the parameter gradients, in the same order of sums in every run.
  * d_o, d_u, d_x are the forward's inputs; without the pre norm d_x is not read.
- * A do or du beyond f16 leaves MTGR_ERR_RANGE in d_status (may be NULL) and an
- * infinity. Workspace: mtgr_boundary_bwd_workspace_bytes (0 on invalid
+ * The parameter gradients add up in fp32 over runs of rows (169 at T = 200003 and d =
+ * 512), then in fp64 over the runs. But for d_dx as d_dh, no output overlaps an input or
+ * another output. A do or du beyond f16 leaves MTGR_ERR_RANGE in d_status (may be
+ * NULL) and an infinity. Workspace: mtgr_boundary_bwd_workspace_bytes (0 on invalid
  * parameters). Timer class MTGR_TIMER_BWD_GLN.
  */
 MTGR_API size_t mtgr_boundary_bwd_workspace_bytes(int32_t T, const mtgr_boundary_params* p);
@@ -750,10 +757,14 @@ MTGR_API int mtgr_quantize_rows(int32_t M, int32_t K, int32_t x_dtype, const voi
  * value beyond 65504 saturates and leaves MTGR_ERR_RANGE in d_status, as an
  * internal wait that ran out leaves MTGR_ERR_TIMEOUT; with d_status NULL both go
  * unseen. q_cols > 0 (a multiple of 32) halves columns [0, q_cols) at the end.
- *   d_a [M][K], d_b [N][K] int8; d_out, d_resid [M][N], distinct buffers
+ * A row's result does not depend on the other rows of the call. SiLU's e^-v is
+ * within 2 + 1.2 |v| fp32 ulp.
+ *   d_a [M][K], d_b [N][K] int8; d_out, d_resid [M][N], distinct buffers; d_out
+ *   overlaps no input
  *   K % 16 == 0, K < 131072, N % 8 == 0, M and N at most 2^30; d_a, d_b, d_b_scale, d_bias, d_resid,
  *   d_out 16-byte aligned
- * Runs on tcgen05. Timer class MTGR_TIMER_GEMM_QKVU, as mtgr_gemm.
+ * Runs on tcgen05, up to 16 rows (and K <= 6336, N <= 32 x SMs) on mma.sync. Timer
+ * class MTGR_TIMER_GEMM_QKVU, as mtgr_gemm.
  */
 MTGR_API int mtgr_gemm_i8(int32_t M, int32_t N, int32_t K, const int8_t* d_a, const float* d_a_scale,
                           const int8_t* d_b, const float* d_b_scale, const float* d_bias, int32_t epi,
@@ -792,8 +803,10 @@ typedef struct mtgr_grad_tensor {
  *   out = g inv_scale min(1, max_norm / (norm + 1e-6))
  * h_grads is a HOST array, read before the call returns; the outputs must not
  * overlap one another, nor a gradient other than their own. Outputs for all
- * tensors, or NULL for all: the norm alone. Sums in fp64, in the same order in
- * every run. A norm that is not finite leaves the outputs untouched and
+ * tensors, or NULL for all: the norm alone. Sums in fp64 over fp32 sums of eight
+ * squares (of single values in fp64 where eight leave fp32's range), in the same
+ * order in every run. An output beyond its type becomes an infinity (inv_scale above
+ * 1 on f16). A norm that is not finite leaves the outputs untouched and
  * MTGR_ERR_RANGE in d_status (a step to skip). max_norm >= 0 (infinity: no
  * clipping), inv_scale > 0 and finite. Workspace: mtgr_grad_clip_workspace_bytes
  * (0 on invalid arguments), zeroed by the caller before its first use; every call
