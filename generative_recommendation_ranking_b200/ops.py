@@ -12,6 +12,7 @@ current stream. The order between the two streams is the caller's: inputs ready 
 from __future__ import annotations
 
 import functools
+import inspect
 from ctypes import byref as _byref
 
 import torch
@@ -29,49 +30,51 @@ _STREAM_TYPES = (torch.float32, torch.bfloat16)
 
 _device_now = torch._C._cuda_getDevice
 _stream_now = torch._C._cuda_getCurrentRawStream
+_set_stream = torch._C._cuda_setStream  # torch.cuda.stream takes about 10 us a use, this 1
 _DENSE = torch.contiguous_format
 
 
-def _on_its_device(fn):
-    """Runs ``fn`` with its first tensor's device as the current one (the library
-    works on the current device)."""
+def _in_its_place(fn):
+    """Runs ``fn`` with its first tensor's device as the current one (the library works
+    on the current device), and its argument ``stream`` as the current stream: what it
+    allocates is then that stream's memory (the caller's may be a buffer that was dropped
+    while work there still runs). Its results are kept from being handed out again before
+    the caller's stream, where their reader is, has got past their release."""
 
-    first = fn.__code__.co_varnames[0]
+    names = list(inspect.signature(fn).parameters)
+    first, at = names[0], names.index("stream")
 
     @functools.wraps(fn)
     def call(*args, **kwargs):
         t = args[0] if args else kwargs.get(first)
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{first}: a device tensor is needed")
-        if t.get_device() == _device_now():
+        dev = t.get_device()
+        if dev != _device_now():
+            with torch.cuda.device(dev):
+                return call(*args, **kwargs)
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None or stream.cuda_stream == _stream_now(dev):
             return fn(*args, **kwargs)
-        with torch.cuda.device(t.device):
-            return fn(*args, **kwargs)
+        if stream.device_index != dev:
+            raise ValueError(f"stream: one of cuda:{dev} is needed, got {stream}")
+        now = torch.cuda.current_stream(dev)
+        _set_stream(stream_id=stream.stream_id, device_index=dev, device_type=stream.device_type)
+        try:
+            out = fn(*args, **kwargs)
+        finally:
+            _set_stream(stream_id=now.stream_id, device_index=dev, device_type=now.device_type)
+        for v in (out,) if isinstance(out, torch.Tensor) else out.values() if isinstance(out, dict) else out:
+            if v is not None:
+                v.record_stream(now)
+        return out
 
     return call
 
 
-def _where(stream, dev: int):
-    """(cudaStream_t, the stream if it is not the current one) of a call."""
-    now = _stream_now(dev)
-    if stream is None or stream.cuda_stream == now:
-        return now, None
-    return stream.cuda_stream, stream
-
-
-def _new(like, other, shape=None, dtype=None, scratch=False) -> torch.Tensor:
-    """A buffer beside ``like``, of its shape and type unless given. One for another
-    stream comes out of that stream's memory (the current stream's may be a buffer that
-    was dropped while its work there still runs), and unless it is scratch, is kept from
-    being handed out again before the current stream, where its reader is, has got past
-    its release. (An existing tensor's allocation is called twice as fast as torch.empty.)"""
-    if other is not None:
-        now = torch.cuda.current_stream(like.device)
-        with torch.cuda.stream(other):
-            t = _new(like, None, shape, dtype)
-        if not scratch:
-            t.record_stream(now)
-        return t
+def _new(like, shape=None, dtype=None) -> torch.Tensor:
+    """A buffer beside ``like``, of its shape and type unless given, on the current
+    stream. (An existing tensor's allocation is called twice as fast as torch.empty.)"""
     if shape is None:
         return torch.empty_like(like, memory_format=_DENSE) if dtype is None else \
             torch.empty_like(like, dtype=dtype, memory_format=_DENSE)
@@ -148,7 +151,7 @@ def _boundary(x, o, u, group_id, values, eps, gate, dev):
     return MtgrBoundaryParams(d, G, eps, code, *ptr), ld_o, ld_u
 
 
-@_on_its_device
+@_in_its_place
 def boundary_forward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=None, pre_gamma=None,
                      pre_beta=None, *, gate="linear", y_dtype=torch.bfloat16, eps: float = EPS, h=None,
                      y=None, y_scale=None, stream=None):
@@ -166,11 +169,11 @@ def boundary_forward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=N
     pre norm, y_scale but for int8. ``h`` may be given as ``x``: in place.
     """
     dev = x.get_device()
-    raw, other = _where(stream, dev)
+    raw = _stream_now(dev)
     p, ld_o, ld_u = _boundary(x, o, u, group_id, (post_gamma, post_beta, scale, pre_gamma, pre_beta), eps, gate, dev)
     shape = x.shape
     if h is None:
-        h = _new(x, other)
+        h = _new(x)
     else:
         _given("h", h, shape, x.dtype, dev)
     if pre_gamma is None:
@@ -179,13 +182,13 @@ def boundary_forward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=N
         if y_dtype not in (torch.float32, torch.bfloat16, torch.int8):
             raise ValueError(f"y_dtype {y_dtype}: float32, bfloat16 or int8")
         if y is None:
-            y = _new(x, other, dtype=y_dtype)
+            y = _new(x, dtype=y_dtype)
         else:
             _given("y", y, shape, y_dtype, dev)
         if y_dtype != torch.int8:
             y_scale = None
         elif y_scale is None:
-            y_scale = _new(pre_gamma, other, shape[0])
+            y_scale = _new(pre_gamma, shape[0])
         else:
             _given("y_scale", y_scale, shape[:1], torch.float32, dev)
     _lib.check("mtgr_boundary_fwd", _lib.load().mtgr_boundary_fwd(
@@ -195,7 +198,7 @@ def boundary_forward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=N
     return h, y, y_scale
 
 
-@_on_its_device
+@_in_its_place
 def boundary_backward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=None, pre_gamma=None,
                       pre_beta=None, dh=None, dy=None, *, gate="linear", eps: float = EPS, ws=None,
                       status=None, stream=None) -> dict:
@@ -207,7 +210,7 @@ def boundary_backward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=
     device int32 word (zeroed by the caller) that tells of f16 gradients out of range.
     """
     dev = x.get_device()
-    raw, other = _where(stream, dev)
+    raw = _stream_now(dev)
     values = (post_gamma, post_beta, scale, pre_gamma, pre_beta)
     p, ld_o, ld_u = _boundary(x, o, u, group_id, values, eps, gate, dev)
     shape = x.shape
@@ -222,16 +225,16 @@ def boundary_backward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=
         raise ValueError("without the pre norm dh is needed, and no dy")
     if status is not None:
         _given("status", status, (1,), torch.int32, dev)
-    dx, do = _new(x, other), _new(o, other)
+    dx, do = _new(x), _new(o)
     out = dict(dx=dx, do=do)
     du = None
     if ld_u:
-        du = out["du"] = _new(o, other)
+        du = out["du"] = _new(o)
     # one allocation for the parameters' gradients
     names = [n for n, v in zip(_PARAMS, values) if v is not None]
     ptr = [None] * 5
     if names:
-        flat = _new(next(v for v in values if v is not None), other, (len(names), p.G, d))
+        flat = _new(next(v for v in values if v is not None), (len(names), p.G, d))
         out.update(zip(names, flat.unbind(0)))
         base, k = flat.data_ptr(), 0
         for i, v in enumerate(values):
@@ -242,7 +245,7 @@ def boundary_backward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=
     room = _given_ws(ws, need, dev)
     if room == 0:
         room = max(need, 256)
-        ws = _new(group_id, other, room, scratch=True)
+        ws = _new(group_id, room)
     _lib.check("mtgr_boundary_bwd", _lib.load().mtgr_boundary_bwd(
         _byref(p), T, group_id.data_ptr(), _CODE[o.dtype], o.data_ptr(), ld_o, u.data_ptr() if ld_u else None, ld_u,
         _CODE[x.dtype], x.data_ptr(), None if dh is None else dh.data_ptr(), 0 if dy is None else _CODE[dy.dtype],
@@ -252,23 +255,23 @@ def boundary_backward(x, o, u, group_id, post_gamma=None, post_beta=None, scale=
     return out
 
 
-@_on_its_device
+@_in_its_place
 def quantize_rows(x, q=None, scale=None, stream=None):
     """Rows of ``x`` [M, K] (float32, bfloat16, float16) to signed bytes with a
     float32 scale each (mtgr_quantize_rows): returns (q [M, K] int8, scale [M]).
     A weight's rows give the scales of its output channels."""
     dev = x.get_device()
-    raw, other = _where(stream, dev)
+    raw = _stream_now(dev)
     if x.dim() != 2:
         raise ValueError("x: [M, K] is needed")
     shape = x.shape
     ld = _given_rows("x", x, shape, _FLOATS, dev)
     if q is None:
-        q = _new(x, other, dtype=torch.int8)
+        q = _new(x, dtype=torch.int8)
     else:
         _given("q", q, shape, torch.int8, dev)
     if scale is None:
-        scale = _new(x, other, shape[0], torch.float32)
+        scale = _new(x, shape[0], torch.float32)
     else:
         _given("scale", scale, shape[:1], torch.float32, dev)
     _lib.check("mtgr_quantize_rows", _lib.load().mtgr_quantize_rows(
@@ -276,7 +279,7 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     return q, scale
 
 
-@_on_its_device
+@_in_its_place
 def linear_i8(x, w, w_scale, x_scale=None, bias=None, epi: int = MTGR_EPI_NONE, resid=None, q_cols: int = 0,
               out_dtype=torch.float32, out=None, ws=None, status=None, stream=None) -> torch.Tensor:
     """Linear layer with int8 weights ``w`` [N, K] and a scale per output channel
@@ -287,7 +290,7 @@ def linear_i8(x, w, w_scale, x_scale=None, bias=None, epi: int = MTGR_EPI_NONE, 
     (zeroed by the caller) for errors the device finds: an f16 value out of
     range, a wait that ran out; without it they go unseen."""
     dev = x.get_device()
-    raw, other = _where(stream, dev)
+    raw = _stream_now(dev)
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x: [M, K] and w: [N, K] are needed")
     M, K = x.shape
@@ -303,7 +306,7 @@ def linear_i8(x, w, w_scale, x_scale=None, bias=None, epi: int = MTGR_EPI_NONE, 
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype {out_dtype}: float32, bfloat16 or float16")
     if out is None:
-        out = _new(w_scale, other, (M, N)) if out_dtype == torch.float32 else _new(w_scale, other, (M, N), out_dtype)
+        out = _new(w_scale, (M, N)) if out_dtype == torch.float32 else _new(w_scale, (M, N), out_dtype)
     else:
         _given("out", out, (M, N), out_dtype, dev)
     if status is not None:
@@ -325,7 +328,7 @@ def linear_i8(x, w, w_scale, x_scale=None, bias=None, epi: int = MTGR_EPI_NONE, 
     room, p = _given_ws(ws, need, dev), None
     if need > 0:
         if room == 0:
-            ws, room = _new(w, other, need, scratch=True), need
+            ws, room = _new(w, need), need
         p = ws.data_ptr()
     _lib.check("mtgr_linear_i8", _lib.load().mtgr_linear_i8(M, N, K, _CODE[x.dtype], x.data_ptr(), ld, *tail, p, room, st,
                                                             raw))
@@ -419,21 +422,21 @@ class GradientSet:
             raise _lib.MTGRError("device status", st)
 
 
-@_on_its_device
+@_in_its_place
 def _clip(ws, grads, table, max_norm, inv_scale, norm, status, stream):
     dev = ws.get_device()
-    raw, other = _where(stream, dev)
+    raw = _stream_now(dev)
     if norm is None:
-        norm = _new(ws, other, 1, torch.float32)
+        norm = _new(ws, 1, torch.float32)
     else:
         _given("norm", norm, (1,), torch.float32, dev)
     if status is None:
         status = grads.status
     else:
         _given("status", status, (1,), torch.int32, dev)
-    if other is not None:
-        ws.record_stream(other)
-        grads.status.record_stream(other)
+    if stream is not None:
+        ws.record_stream(stream)
+        grads.status.record_stream(stream)
     _lib.check("mtgr_grad_clip", _lib.load().mtgr_grad_clip(
         table, len(table), max_norm, inv_scale, norm.data_ptr(), ws.data_ptr(), ws.numel(), status.data_ptr(), raw))
     return norm
