@@ -2,6 +2,7 @@
 against the same call made plainly. Tolerances: tests/test_gpu_operators.py."""
 
 import threading
+import types
 
 import numpy as np
 import pytest
@@ -476,3 +477,12 @@ def test_clip_factors_below_the_normal_numbers(sizes, dtype, to, scale, max_norm
         tol = 128 * 2.0 ** -24 * np.abs(w) + HALF[to] * np.abs(w) * 1.001 + (tiny if to == torch.float32 else 2.0 ** -133)
         assert (np.abs(host(o) - w) <= tol).all(), (np.abs(host(o) - w) / np.maximum(np.abs(w), 1e-300)).max()
     plan.check()
+
+
+def test_a_stream_of_another_device_is_refused():
+    x = torch.randn(4, 64, device="cuda")
+    elsewhere = types.SimpleNamespace(cuda_stream=0x1234, device_index=torch.cuda.current_device() + 1)
+    for call in (lambda: mt.quantize_rows(x, stream=elsewhere), lambda: mt.quantize_rows(x, None, None, elsewhere),
+                 lambda: mt.GradientSet([x]).clip(1.0, stream=elsewhere)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
