@@ -3,8 +3,8 @@ into the C ABI. Every step of the forward runs in the library's CUDA kernels;
 this module only sizes and allocates buffers and marshals arguments.
 
 With ``stream`` a call works on that stream and allocates its memory; the order
-with other streams is the caller's: inputs ready for ``stream`` before the call,
-results read behind it.
+with other streams is the caller's: inputs ready for ``stream`` before the call and
+kept until it has run, results read behind it.
 """
 
 from __future__ import annotations

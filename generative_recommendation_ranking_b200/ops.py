@@ -6,7 +6,8 @@ ABI on ``stream`` (default: the device's current stream). What it allocates is
 ``stream``'s own memory, so nothing that still runs on another stream uses it, and
 it may be dropped while the work runs on ``stream`` or its results are read on the
 current stream. The order between the two streams is the caller's: inputs ready for
-``stream`` before the call, results read behind it.
+``stream`` before the call and kept until it has run, results read behind it. Outputs
+and workspaces that are given overlap no input, but where a docstring says so.
 """
 
 from __future__ import annotations

@@ -486,3 +486,27 @@ def test_a_stream_of_another_device_is_refused():
                  lambda: mt.GradientSet([x]).clip(1.0, stream=elsewhere)):
         with pytest.raises(ValueError, match="stream"):
             call()
+
+
+@pytest.mark.parametrize("kind", ["default", "external", "priority"])
+def test_streams_of_every_kind(kind):
+    # the default stream while another is current, one made elsewhere, one of high priority
+    x = torch.randn(300, 512, device="cuda")
+    w, ws = mt.quantize_rows(torch.randn(64, 512, device="cuda"))
+    want = mt.linear_i8(x, w, ws)
+    raw = torch.cuda.Stream()
+    stream = {"default": torch.cuda.default_stream(), "external": torch.cuda.ExternalStream(raw.cuda_stream),
+              "priority": torch.cuda.Stream(priority=-1)}[kind]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        now = torch.cuda.current_stream()
+        got = mt.linear_i8(x, w, ws, stream=stream)
+        norm = mt.GradientSet([x]).norm(stream=stream)
+        y = mt.gemm(x.bfloat16(), x[:64].bfloat16(), stream=stream) if kind == "default" else None
+        assert torch.cuda.current_stream() == now
+        with pytest.raises(ValueError):
+            mt.linear_i8(x, w, ws, out_dtype=torch.int8, stream=stream)  # refused: the stream is put back
+        assert torch.cuda.current_stream() == now
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and abs(norm.item() - x.double().norm().item()) <= 1e-5 * norm.item()
+    assert y is None or y.shape == (300, 64)
